@@ -4,6 +4,10 @@
 * ``merge``     exact (O, LSE) merge of two key-chunk partials (Ring Attention step)
 * ``seq2head``  Ulysses sequence shards -> head groups over P virtual ranks
 * ``head2seq``  the inverse permute
+* ``window_fwd`` / ``window_decode``  attention limited to a window and the first tokens, over
+  key chunks or a serving cache
+* ``rope`` / ``qk_norm_rope`` / ``seq2head_qkv_norm_rope``  rotary positions: alone, with the
+  Q/K RMSNorm, and with both fused into the Ulysses re-partition
 * ``ring_attention`` / ``ulysses_attention``  the two per-rank compositions
 * ``UlyssesHostPass``  a whole Ulysses layer from host shards to host O/LSE, copies
   pipelined with the attention inside the library (cpattn_ulysses_host)
@@ -30,14 +34,21 @@ from ._binding import (  # noqa: F401
     lib,
     library_path,
     merge,
+    qk_norm_rope,
     rmsnorm,
+    rope,
+    rope_axes,
+    rope_frequencies,
     selftest_exp2,
     selftest_wait_timeout,
     seq2head,
     seq2head_qkv,
     seq2head_qkv_norm,
+    seq2head_qkv_norm_rope,
     status_str,
     version,
+    window_decode,
+    window_fwd,
 )
 from .paths import (  # noqa: F401
     UlyssesHostPass,

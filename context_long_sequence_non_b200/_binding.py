@@ -69,6 +69,13 @@ def lib() -> ctypes.CDLL:
             L.cpattn_rmsnorm.argtypes = [vp, vp, vp, i, i, f, f, vp]
             L.cpattn_seq2head_qkv_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f,
                                                    f, vp]
+            d = ctypes.c_double
+            L.cpattn_window_fwd.argtypes = [vp] * 6 + [i] * 6 + [ll] * 3 + [f] + [i] * 8 + [vp]
+            L.cpattn_window_decode.argtypes = [vp] * 6 + [i] * 6 + [ll] * 3 + [f] + [i] * 4 + [vp]
+            L.cpattn_rope_frequencies.argtypes = [vp, vp, i, d, i, d, d, d, d]
+            L.cpattn_rope.argtypes = [vp] * 4 + [i] * 7 + [f, ll, ll, i, vp]
+            L.cpattn_qk_norm_rope.argtypes = [vp] * 8 + [i] * 8 + [f] * 3 + [ll] * 4 + [i, vp]
+            L.cpattn_seq2head_qkv_norm_rope.argtypes = [vp] * 10 + [i] * 7 + [f] * 3 + [vp]
             L.cpattn_status_str.argtypes = [i]
             L.cpattn_status_str.restype = ctypes.c_char_p
             L.cpattn_device_error.argtypes = []
@@ -79,7 +86,9 @@ def lib() -> ctypes.CDLL:
                          "cpattn_ulysses_fwd_split", "cpattn_ulysses_host",
                          "cpattn_fwd_split", "cpattn_split_suggest", "cpattn_merge", "cpattn_seq2head_qkv", "cpattn_seq2head", "cpattn_head2seq",
                          "cpattn_device_error", "cpattn_selftest_wait_timeout", "cpattn_version",
-                         "cpattn_selftest_exp2"):
+                         "cpattn_selftest_exp2", "cpattn_window_fwd", "cpattn_window_decode",
+                         "cpattn_rope_frequencies", "cpattn_rope", "cpattn_qk_norm_rope",
+                         "cpattn_seq2head_qkv_norm_rope"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -417,6 +426,266 @@ def head2seq(src, P, out=None, stream=None):
     st = lib().cpattn_head2seq(_ptr(src), _ptr(out), P, S_l, H, D, src.element_size(),
                                _stream(stream))
     _check(st, "cpattn_head2seq")
+    return out
+
+
+# ------------------------------------------------------------------ windowed attention
+
+
+def _call(device, stream, what, fn, *args):
+    """Run a library call with ``device`` current (the library launches on the current device)
+    on ``stream``, or on that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    if st != OK:
+        raise CpattnError(st, what)
+
+
+def _same_device(first, *ts):
+    if not first.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors must live on one CUDA device")
+
+
+def _token_stride(t, name, dims=4):
+    """Elements between consecutive tokens of a [..., tokens, heads, D] tensor whose heads are
+    packed and whose tokens are evenly spaced through every leading axis."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims and dims:
+        raise ValueError(f"{name} must have {dims} axes")
+    D, H = shape[-1], shape[-2]
+    if t.numel() == 0:
+        return H * D
+    if (D > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    step, count = None, 1  # `count` tokens below this axis, `step` apart once one axis shows it
+    for n, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if n > 1:
+            if step is None:
+                if st % count:
+                    raise ValueError(f"{name}: tokens must be evenly spaced")
+                step = st // count
+            elif st != step * count:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+        count *= n
+    if step is None:
+        return H * D
+    if step < H * D:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return step
+
+
+def _packed(t, shape, name, dtype):
+    _need_shape(t, shape, name, dtype)
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _extent(n, name, least=-(1 << 31)):
+    n = int(n)
+    if not least <= n < 1 << 31:
+        raise ValueError(f"{name} is out of range")
+    return n
+
+
+def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [B][S][H][D]")
+    B, Sq, H, D = q.shape
+    Skv, Hkv = k.shape[1], k.shape[2]
+    if k.shape != (B, Skv, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [B][Skv][Hkv][D] matching q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one dtype")
+    strides = tuple(_token_stride(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    if kv_len is not None:
+        _packed(kv_len, (B,), "kv_len", torch.int32)
+    if out is None:
+        out = torch.empty((B, Sq, H, D), dtype=out_dtype or q.dtype, device=q.device)
+    else:
+        _packed(out, (B, Sq, H, D), "out", out_dtype)
+    if lse is not None:
+        _packed(lse, (B, H, Sq), "lse", torch.float32)
+    elif want_lse:
+        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+    _same_device(q, k, v, kv_len, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr())
+    return ptrs, (B, H, Hkv, Sq, Skv, D), strides, float(scale), out, lse
+
+
+def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=None, out=None,
+               lse=None, scale=None, out_dtype=None, want_lse=True, accumulate=False, stream=None):
+    """Attention limited to a window: the query at position p = q_pos + i sees the keys at
+    positions p - left .. p + right (-1: no bound on that side) and, up to p + right, those below
+    ``sinks``; see cpattn_window_fwd.
+
+    q: [B][Sq][H][D], k/v: [B][Skv][Hkv][D] with H a multiple of Hkv (bf16 -> tensor-core kernel,
+    D 64 or 128; fp32 -> CUDA-core kernel, D <= 256); their heads may be slices of a wider row.
+    ``kv_len``: int32 [B], keys of each sequence.  ``accumulate`` merges into the running
+    (out, lse).  Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
+    if accumulate and (out is None or lse is None):
+        raise ValueError("accumulate needs the running out and lse")
+    ptrs, dims, strides, scale, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype,
+                                                        want_lse)
+    _call(q.device, stream, "cpattn_window_fwd", lib().cpattn_window_fwd, *ptrs, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
+          *dims, *strides, scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
+          _extent(left, "left"), _extent(right, "right"), _extent(sinks, "sinks"),
+          _dtype_code(q.dtype), _dtype_code(out.dtype), 1 if accumulate else 0)
+    return out, lse
+
+
+def window_decode(q, k_cache, v_cache, kv_len=None, left=-1, sinks=0, out=None, lse=None, scale=None,
+                  out_dtype=None, want_lse=True, stream=None):
+    """The last Sq tokens of each sequence against its cache (causal, window and sinks as
+    window_fwd): q [B][Sq][H][D], caches [B][S_max][Hkv][D], ``kv_len`` int32 [B] the tokens each
+    sequence holds, the newest included (None: S_max).  See cpattn_window_decode."""
+    ptrs, dims, strides, scale, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale,
+                                                        out_dtype, want_lse)
+    _call(q.device, stream, "cpattn_window_decode", lib().cpattn_window_decode, *ptrs,
+          None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
+          None if lse is None else lse.data_ptr(), *dims, *strides, scale, _extent(left, "left"),
+          _extent(sinks, "sinks"), _dtype_code(q.dtype), _dtype_code(out.dtype))
+    return out, lse
+
+
+# ------------------------------------------------------------------ rotary positions
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def rope_frequencies(rot, base=10000.0, scaling="plain", stretch=1.0, train_len=0.0, beta_fast=32.0,
+                     beta_slow=1.0, device="cpu"):
+    """``(freq float64 [rot/2], factor)``: radians per position of each rotated pair and the
+    factor on the rotated part, see cpattn_rope_frequencies."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {tuple(ROPE_SCALING)}")
+    rot = _extent(rot, "rot")
+    freq = torch.empty(max(rot // 2, 0), dtype=torch.float64)
+    factor = ctypes.c_float()
+    _check(lib().cpattn_rope_frequencies(freq.data_ptr(), ctypes.addressof(factor), rot, float(base),
+                                         ROPE_SCALING[scaling], float(stretch), float(train_len),
+                                         float(beta_fast), float(beta_slow)),
+           "cpattn_rope_frequencies")
+    return freq.to(device), factor.value
+
+
+def rope_axes(freqs):
+    """[axes][rot/2] frequencies of a multi-axis rotation: axis a turns its own run of pairs with
+    the frequencies ``freqs[a]``, the runs in order."""
+    n = sum(f.numel() for f in freqs)
+    out = torch.zeros(len(freqs), n, dtype=torch.float64, device=freqs[0].device)
+    at = 0
+    for a, f in enumerate(freqs):
+        out[a, at:at + f.numel()] = f
+        at += f.numel()
+    return out
+
+
+def _rope_args(tokens, pos, freq):
+    if freq.dtype != torch.float64 or freq.dim() not in (1, 2) or not freq.is_contiguous():
+        raise ValueError("freq must be a contiguous float64 [rot/2] or [axes][rot/2]")
+    axes = 1 if freq.dim() == 1 else freq.shape[0]
+    if pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ValueError("pos must be contiguous int32")
+    if axes == 0 or pos.numel() % axes or (pos.dim() > 1 and pos.shape[-1] != axes) or (
+            pos.dim() < 2 and axes > 1):
+        raise ValueError("pos must be [rows] or [..., rows, axes] matching freq")
+    rows = pos.numel() // axes
+    if tokens and (rows < 1 or tokens % rows):
+        raise ValueError("the tokens must be a multiple of pos's rows")
+    return rows, axes, 2 * freq.shape[-1]
+
+
+def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
+    """Rotary positions of x [..., tokens, H, D] (bf16 or fp32): the first rot elements of every
+    head turn by ``pos @ freq`` (pos int32 [rows] or [rows][axes], freq float64 [rot/2] or
+    [axes][rot/2]); ``out=x`` rotates in place.  See cpattn_rope."""
+    if x.dim() < 3:
+        raise ValueError("x must be [..., tokens, H, D]")
+    H, D = x.shape[-2:]
+    tokens = x.shape[:-2].numel()
+    rows, axes, rot = _rope_args(tokens, pos, freq)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need_shape(out, x.shape, "out", x.dtype)
+    _same_device(x, pos, freq, out)
+    _call(x.device, stream, "cpattn_rope", lib().cpattn_rope, x.data_ptr(), out.data_ptr(),
+          pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes, 1 if interleaved else 0,
+          float(factor), _token_stride(x, "x", 0), _token_stride(out, "out", 0), _dtype_code(x.dtype))
+    return out
+
+
+def qk_norm_rope(q, k, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.0, eps=1e-6,
+                 out_scale=1.0, out=None, stream=None):
+    """RMSNorm (weights float32 [D]) and rotary positions of query heads q [..., tokens, Hq, D]
+    and key heads k [..., tokens, Hk, D] in one pass; ``out`` is an optional (q, k) pair, which
+    may be (q, k) themselves.  See cpattn_qk_norm_rope."""
+    if q.dim() < 3 or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1] or q.dtype != k.dtype:
+        raise ValueError("q and k must be [..., tokens, H, D] of the same tokens, D and dtype")
+    D = q.shape[-1]
+    tokens = q.shape[:-2].numel()
+    for g in (gamma_q, gamma_k):
+        if g.dtype != torch.float32 or g.shape != (D,) or not g.is_contiguous():
+            raise ValueError("gamma_q and gamma_k must be float32 [D]")
+    rows, axes, rot = _rope_args(tokens, pos, freq)
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    qo, ko = out
+    _need_shape(qo, q.shape, "out[0]", q.dtype)
+    _need_shape(ko, k.shape, "out[1]", k.dtype)
+    _same_device(q, k, gamma_q, gamma_k, pos, freq, qo, ko)
+    _call(q.device, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope, q.data_ptr(),
+          k.data_ptr(), qo.data_ptr(), ko.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(),
+          pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2], k.shape[-2], D, rot, axes,
+          1 if interleaved else 0, float(eps), float(out_scale), float(factor),
+          _token_stride(q, "q", 0), _token_stride(k, "k", 0), _token_stride(qo, "out[0]", 0),
+          _token_stride(ko, "out[1]", 0), _dtype_code(q.dtype))
+    return qo, ko
+
+
+def seq2head_qkv_norm_rope(q, k, v, P, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.0,
+                           eps=1e-6, out_scale=1.0, out=None, stream=None):
+    """seq2head of Q, K, V in one launch with Q and K head rows normalised (weights float32 [D];
+    both None: not) and rotated on the way; pos [P*S_l] or [P*S_l][axes] in the order of the full
+    sequence.  ``out`` is an optional (qh, kh, vh) triple.  See cpattn_seq2head_qkv_norm_rope."""
+    if q.dim() != 4 or q.shape[0] != P or k.shape != q.shape or v.shape != q.shape or any(
+            t.dtype != torch.bfloat16 for t in (q, k, v)):
+        raise ValueError("q, k, v must be same-shaped bf16 [P][S_l][H][D] tensors")
+    P, S_l, H, D = q.shape
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k go together")
+    for g in (gamma_q, gamma_k):
+        if g is not None and (g.dtype != torch.float32 or g.shape != (D,) or not g.is_contiguous()):
+            raise ValueError("gamma_q and gamma_k must be float32 [D]")
+    rows, axes, rot = _rope_args(P * S_l, pos, freq)
+    if rows != P * S_l:
+        raise ValueError("pos must have a row for every token of the full sequence")
+    grouped = (P, P * S_l, H // P, D)
+    if out is None:
+        out = tuple(torch.empty(grouped, dtype=q.dtype, device=q.device) for _ in range(3))
+    for i, t in enumerate(out):
+        _packed(t, grouped, f"out[{i}]", q.dtype)
+    for t in (q, k, v):
+        if not t.is_contiguous():
+            raise ValueError("q, k, v must be contiguous")
+    _same_device(q, k, v, gamma_q, gamma_k, pos, freq, *out)
+    _call(q.device, stream, "cpattn_seq2head_qkv_norm_rope", lib().cpattn_seq2head_qkv_norm_rope,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out),
+          None if gamma_q is None else gamma_q.data_ptr(),
+          None if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H,
+          D, rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor))
     return out
 
 

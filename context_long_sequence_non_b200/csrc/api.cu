@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api_common.h"
 #include "cpattn.h"
 #include "kernels.h"
 #include "sm100_ptx.cuh"
@@ -18,6 +19,10 @@ namespace {
 __device__ int g_cpattn_err;
 
 constexpr int kMaxDevices = 64;
+
+}  // namespace
+
+namespace cpattn {
 
 int* device_error_word() {
   static int* addr[kMaxDevices] = {nullptr};
@@ -33,7 +38,7 @@ int* device_error_word() {
   return addr[dev];
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -46,11 +51,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace cpattn
+
+namespace {
+
+using cpattn::aligned;
+using cpattn::cuda_status;
+using cpattn::device_error_word;
+using cpattn::elem_size;
+using cpattn::overlap;
+
 // [B][S][H][D] bf16 tensor, box = 64 head-dim columns x 1 head x `box_rows` tokens x 1
 // batch, 128-byte swizzle (the layout tcgen05 reads through a 128-byte-swizzle descriptor).
 bool encode_bshd_bf16(CUtensorMap* map, const void* ptr, int B, int S, int H, int D,
                       unsigned box_rows = 128) {
-  auto fn = encode_fn();
+  auto fn = cpattn::tensor_map_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(S), cuuint64_t(B)};
   const cuuint64_t strides[3] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2,
@@ -63,17 +78,6 @@ bool encode_bshd_bf16(CUtensorMap* map, const void* ptr, int B, int S, int H, in
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA; }
-
-int elem_size(int dtype) { return dtype == CPATTN_BF16 ? 2 : (dtype == CPATTN_F32 ? 4 : 0); }
 
 }  // namespace
 

@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "kernels.h"
+#include "norm_math.cuh"
 #include "sm100_ptx.cuh"
 
 namespace cpattn {
@@ -463,16 +464,6 @@ struct RowNorm {
   int row_vec;
   float inv_d, eps, out_scale;
 };
-
-// 1/sqrt(a) for a > 0: the special-function unit's estimate refined by one Newton step on
-// f(y) = 1/y^2 - a (y' = y * (3 - a y^2) / 2), which brings it to about an ulp of the
-// float32 1/sqrt(a) for every positive finite a (subnormal a included).
-__device__ __forceinline__ float rsqrt_refined(float a) {
-  float y;
-  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(a));
-  const float hy = 0.5f * y;
-  return fmaf(hy, fmaf(-a * y, y, 1.0f), y);  // y + (y/2)(1 - a y^2)
-}
 
 __device__ __forceinline__ void load_gamma8(const float* __restrict__ gamma, int d0, float (&g)[8]) {
   const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + d0));

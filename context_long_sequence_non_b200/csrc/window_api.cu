@@ -1,0 +1,113 @@
+// window_api.cu -- the C entry points of windowed attention and its single-token form:
+// argument checks (all before the first CUDA call) and dispatch.
+#include <cmath>
+#include <cstdint>
+
+#include "api_common.h"
+#include "cpattn.h"
+#include "kernels.h"
+#include "window.h"
+
+using cpattn::aligned;
+using cpattn::cuda_status;
+using cpattn::elem_size;
+using cpattn::overlap;
+using cpattn::WindowCall;
+
+namespace {
+
+constexpr int kMaxPos = 1 << 30;  // positions stay below this, so position arithmetic fits an int
+
+int clamp_extent(int n) { return n < 0 ? -1 : (n >= kMaxPos ? kMaxPos - 1 : n); }
+
+// Bytes from the first to the last element of n tokens of `row` elements each, `stride` apart.
+size_t span_bytes(long long tokens, long long stride, long long row, int es) {
+  return tokens < 1 ? 0 : size_t((tokens - 1) * stride + row) * es;
+}
+
+// Checks shared by both calls; fills the strides in (0: packed).
+int check(WindowCall* c, int in_dtype, int out_dtype) {
+  if (c->B < 1 || c->H < 1 || c->Hkv < 1 || c->Sq < 1 || c->Skv < 0 || c->D < 1) return CPATTN_ERR_SHAPE;
+  if (c->H % c->Hkv != 0 || c->B > 65535 || c->H > 65535) return CPATTN_ERR_SHAPE;
+  if (c->Sq >= kMaxPos || c->Skv >= kMaxPos) return CPATTN_ERR_SHAPE;
+  if ((long long)c->B * c->Sq * c->H > 0x7fffffffLL) return CPATTN_ERR_SHAPE;  // 32-bit row index
+  if (!(std::isfinite(c->scale) && c->scale > 0.f) || c->sinks < 0) return CPATTN_ERR_SHAPE;
+  const int es = elem_size(in_dtype), oes = elem_size(out_dtype);
+  if (es == 0 || oes == 0) return CPATTN_ERR_UNSUPPORTED;
+  if (in_dtype == CPATTN_BF16 && c->D != 64 && c->D != 128) return CPATTN_ERR_UNSUPPORTED;
+  if (in_dtype == CPATTN_F32 && c->D > 256) return CPATTN_ERR_UNSUPPORTED;
+  if (c->accumulate && in_dtype != CPATTN_BF16) return CPATTN_ERR_UNSUPPORTED;
+  const long long q_row = (long long)c->H * c->D, kv_row = (long long)c->Hkv * c->D;
+  if (c->q_stride == 0) c->q_stride = q_row;
+  if (c->k_stride == 0) c->k_stride = kv_row;
+  if (c->v_stride == 0) c->v_stride = kv_row;
+  const long long most = 1LL << 36;  // elements: 2^37 bytes, inside a tensor map's 40-bit stride
+  if (c->q_stride < q_row || c->k_stride < kv_row || c->v_stride < kv_row || c->q_stride > most ||
+      c->k_stride > most || c->v_stride > most)
+    return CPATTN_ERR_SHAPE;
+  if (c->q == nullptr || c->out == nullptr || (c->accumulate && c->lse == nullptr)) return CPATTN_ERR_NULL;
+  if (c->Skv > 0 && (c->k == nullptr || c->v == nullptr)) return CPATTN_ERR_NULL;
+  if (!aligned(c->q, 16) || !aligned(c->out, 16) || (c->lse != nullptr && !aligned(c->lse, 4)) ||
+      (c->kv_len != nullptr && !aligned(c->kv_len, 4)) ||
+      (c->Skv > 0 && (!aligned(c->k, 16) || !aligned(c->v, 16))))
+    return CPATTN_ERR_ALIGN;
+  if (in_dtype == CPATTN_BF16 && (c->q_stride % 8 || c->k_stride % 8 || c->v_stride % 8))
+    return CPATTN_ERR_ALIGN;  // 16-byte token rows
+  // the outputs are written while the inputs are still read
+  const size_t ob = size_t(c->B) * c->Sq * c->H * c->D * oes, lb = size_t(c->B) * c->H * c->Sq * 4;
+  const size_t qb = span_bytes((long long)c->B * c->Sq, c->q_stride, q_row, es);
+  const size_t kb = span_bytes((long long)c->B * c->Skv, c->k_stride, kv_row, es);
+  const size_t vb = span_bytes((long long)c->B * c->Skv, c->v_stride, kv_row, es);
+  const void* in[3] = {c->q, c->k, c->v};
+  const size_t in_b[3] = {qb, kb, vb};
+  for (int t = 0; t < 3; ++t)
+    if (in_b[t] > 0 && (overlap(c->out, ob, in[t], in_b[t]) ||
+                        (c->lse != nullptr && overlap(c->lse, lb, in[t], in_b[t]))))
+      return CPATTN_ERR_SHAPE;
+  if (c->lse != nullptr && overlap(c->out, ob, c->lse, lb)) return CPATTN_ERR_SHAPE;
+  if (c->kv_len != nullptr && (overlap(c->out, ob, c->kv_len, size_t(c->B) * 4) ||
+                               (c->lse != nullptr && overlap(c->lse, lb, c->kv_len, size_t(c->B) * 4))))
+    return CPATTN_ERR_SHAPE;
+  c->in_f32 = in_dtype == CPATTN_F32;
+  c->out_f32 = out_dtype == CPATTN_F32;
+  return CPATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                      const int* kv_len, int B, int H, int Hkv, int Sq, int Skv, int D,
+                      long long q_stride, long long k_stride, long long v_stride, float scale,
+                      int q_pos, int k_pos, int left, int right, int sinks, int in_dtype,
+                      int out_dtype, int accumulate, cpattn_stream_t stream) {
+  WindowCall c{q, k, v, out, lse, kv_len, B, H, Hkv, Sq, Skv, D, q_stride, k_stride, v_stride, scale,
+               0, clamp_extent(left), clamp_extent(right), sinks, false, false, false, accumulate != 0};
+  const int st = check(&c, in_dtype, out_dtype);
+  if (st != CPATTN_OK) return st;
+  if (q_pos < 0 || k_pos < 0 || q_pos >= kMaxPos - Sq || k_pos >= kMaxPos - Skv) return CPATTN_ERR_SHAPE;
+  c.off = q_pos - k_pos;
+  c.sinks = sinks <= k_pos ? 0 : (sinks - k_pos < Skv ? sinks - k_pos : Skv);
+  // a chunk that no row can see adds nothing to a running result
+  const int last = c.off + Sq - 1;
+  const bool none = Skv == 0 || (c.right >= 0 && last + c.right < 0) ||
+                    (c.left >= 0 && c.sinks == 0 && c.off - c.left >= Skv);
+  if (c.accumulate && none) return CPATTN_OK;
+  return cuda_status(cpattn::launch_window_rows(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache, const int* kv_len,
+                         void* out, float* lse, int B, int H, int Hkv, int Sq, int S_max, int D,
+                         long long q_stride, long long k_stride, long long v_stride, float scale,
+                         int left, int sinks, int in_dtype, int out_dtype, cpattn_stream_t stream) {
+  WindowCall c{q, k_cache, v_cache, out, lse, kv_len, B, H, Hkv, Sq, S_max, D, q_stride, k_stride,
+               v_stride, scale, 0, clamp_extent(left), 0, sinks, true, false, false, false};
+  const int st = check(&c, in_dtype, out_dtype);
+  if (st != CPATTN_OK) return st;
+  if (S_max < 1) return CPATTN_ERR_SHAPE;
+  if (sinks > S_max) c.sinks = S_max;
+  return cuda_status(cpattn::launch_window_rows(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -20,7 +20,7 @@ from . import _binding as B
 
 
 def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True, n_split=1,
-                   stream=None):
+                   stream=None, left=-1, right=-1, sinks=0, q_pos=0, k_pos=None):
     """One rank's ring step over K/V chunks in ring order.
 
     q: [B][Sq][H][D]; each chunk [B][S_c][H][D].  The running (O, LSE) is kept in
@@ -31,12 +31,29 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
     many key ranges folded straight into the accumulator (split-KV, for query slices too
     small to fill the GPU), and ``n_split = 0`` splits only the work items of each chunk's
     last wave or two of CTAs, as the library's makespan model chooses (tail split).
-    Returns ``(O, LSE)``.
+    A window (``left`` or ``right`` not -1; see window_fwd) takes the queries at positions
+    ``q_pos`` on and chunk c at ``k_pos[c]`` on (None: the chunks follow one another from 0);
+    every chunk is then one cpattn_window_fwd, merged in its epilogue, and K/V may have fewer
+    heads than Q.  Returns ``(O, LSE)``.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[3])
     acc_dtype = acc_dtype or q.dtype
     Bn, Sq, H, D = q.shape
+    if left >= 0 or right >= 0:
+        if not fused or n_split != 1:
+            raise ValueError("a windowed ring step is fused and not split")
+        if k_pos is None:
+            k_pos, at = [], 0
+            for kc in k_chunks:
+                k_pos.append(at)
+                at += kc.shape[1]
+        acc_o = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
+        acc_l = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
+        for c, (kc, vc) in enumerate(zip(k_chunks, v_chunks)):
+            B.window_fwd(q, kc, vc, left=left, right=right, sinks=sinks, q_pos=q_pos, k_pos=k_pos[c],
+                         out=acc_o, lse=acc_l, scale=scale, accumulate=c > 0, stream=stream)
+        return acc_o, acc_l
     acc_o = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
     acc_l = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
     if fused:
@@ -75,7 +92,11 @@ class UlyssesPlan:
     """
 
     def __init__(self, P, S_local, H, D, dtype=torch.bfloat16, device="cuda", batched=False,
-                 qk_norm=None, norm_eps=1e-6):
+                 qk_norm=None, norm_eps=1e-6, rope=None, window=None):
+        # rope: (pos, freq) or (pos, freq, interleaved, factor), pos over the full sequence: Q and
+        # K are rotated in the re-partition's launch, after the norm when there is one
+        self.rope = rope
+        self.window = window  # (left, right, sinks) of a windowed pass (cpattn_window_fwd)
         self.batched = batched  # one seq2head launch for Q, K, V together
         # (gamma_q, gamma_k) float32 [D]: the sample's Q/K RMSNorm fused into that launch
         self.qk_norm, self.norm_eps = qk_norm, norm_eps
@@ -92,7 +113,12 @@ class UlyssesPlan:
 
     def run(self, q_shards, k_shards, v_shards, scale=None, stream=None):
         P = self.P
-        if self.qk_norm is not None:
+        if self.rope is not None:
+            gq, gk = self.qk_norm if self.qk_norm is not None else (None, None)
+            B.seq2head_qkv_norm_rope(q_shards, k_shards, v_shards, P, gq, gk, *self.rope,
+                                     eps=self.norm_eps, out=(self.qh, self.kh, self.vh),
+                                     stream=stream)
+        elif self.qk_norm is not None:
             B.seq2head_qkv_norm(q_shards, k_shards, v_shards, P, *self.qk_norm, eps=self.norm_eps,
                                 out=(self.qh, self.kh, self.vh), stream=stream)
         elif self.batched:
@@ -102,7 +128,12 @@ class UlyssesPlan:
             B.seq2head(q_shards, P, out=self.qh, stream=stream)
             B.seq2head(k_shards, P, out=self.kh, stream=stream)
             B.seq2head(v_shards, P, out=self.vh, stream=stream)
-        B.fwd(self.qh, self.kh, self.vh, out=self.oh, lse=self.lse, scale=scale, stream=stream)
+        if self.window is not None:
+            left, right, sinks = self.window
+            B.window_fwd(self.qh, self.kh, self.vh, left=left, right=right, sinks=sinks, out=self.oh,
+                         lse=self.lse, scale=scale, stream=stream)
+        else:
+            B.fwd(self.qh, self.kh, self.vh, out=self.oh, lse=self.lse, scale=scale, stream=stream)
         B.head2seq(self.oh, P, out=self.out, stream=stream)
         return self.out, self.lse
 

@@ -368,6 +368,138 @@ CPATTN_API int cpattn_seq2head_qkv_norm(const void* q, const void* k, const void
 CPATTN_API int cpattn_head2seq(const void* src, void* dst, int P, int S_local, int H, int D,
                     int elem_bytes, cpattn_stream_t stream);
 
+/*
+ * cpattn_window_fwd -- attention limited to a window around each query's position and the
+ * first `sinks` positions of the sequence, with its log-sum-exp.  Long-sequence counterpart of
+ * cpattn_fwd (AllGather KV and Ring Attention sections, Figs. 2-3): same layouts, same (O, LSE)
+ * convention, so the results of key chunks fold with cpattn_merge or with `accumulate`.
+ * Query row i is at position p = q_pos + i and key row j at position t = k_pos + j; key j is
+ * visible to row i when
+ *   j < len(b)  and  (right < 0 or t <= p + right)  and  (left < 0 or t >= p - left or t < sinks)
+ * with len(b) = Skv, or kv_len[b] clamped to 0..Skv.  right = 0 is causal; left = right = w is
+ * a two-sided band; left < 0 and right < 0 lift the bound on that side.  Then
+ *   lse[b,h,i] = ln sum_visible exp(scale q.k),  out = sum_visible exp(scale q.k - lse) v.
+ * A row that sees no key gets out = 0 and lse = -inf.
+ *
+ * q : [B][Sq][H][D], k and v : [B][Skv][Hkv][D], H a multiple of Hkv: query head h uses key head
+ *   h / (H / Hkv).  q_stride, k_stride, v_stride: elements between consecutive tokens, 0 for
+ *   packed rows (H*D or Hkv*D); a larger stride takes heads out of a wider row, such as one
+ *   projection's output.  Consecutive batches are Sq (Skv) such tokens apart.  bf16 strides are
+ *   multiples of 8 (CPATTN_ERR_ALIGN).
+ * out : [B][Sq][H][D] packed, lse : [B][H][Sq] float32, or NULL to skip it.
+ * kv_len : B ints in device memory, or NULL.  Rows of k and v at or past the length are never
+ *   used, whatever they hold (NaN included), and neither are rows that no query of the call
+ *   sees.  A key that some query of the call sees must have finite k and v.
+ * accumulate = 1 (bf16 inputs) merges the result into the running (out, lse) in place as
+ *   cpattn_fwd_accumulate does; a row that sees no key keeps its running (out, lse), and a row
+ *   whose running lse is -inf takes the new result without reading `out`.
+ * 0 <= q_pos, k_pos; q_pos + Sq and k_pos + Skv below 2^30; sinks >= 0; B*Sq*H < 2^31.
+ * in_dtype CPATTN_BF16: D 64 or 128; CPATTN_F32: D <= 256.  out_dtype BF16 or F32.
+ * out and lse must not overlap any input.
+ * Errors: CPATTN_ERR_NULL, _SHAPE, _ALIGN, _UNSUPPORTED, _CUDA; a bounded wait that runs out is
+ *   reported by cpattn_device_error().
+ */
+CPATTN_API int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                                 const int* kv_len, int B, int H, int Hkv, int Sq, int Skv, int D,
+                                 long long q_stride, long long k_stride, long long v_stride,
+                                 float scale, int q_pos, int k_pos, int left, int right, int sinks,
+                                 int in_dtype, int out_dtype, int accumulate, cpattn_stream_t stream);
+
+/*
+ * cpattn_window_decode -- the serving form of cpattn_window_fwd: the last Sq tokens of each
+ * sequence (one, or a few drafted ahead) against its key/value cache.  Sequence b holds
+ * L = kv_len[b] tokens (clamped to 0..S_max; S_max when kv_len is NULL), the newest included;
+ * query row i is its token L - Sq + i, and sees the cache rows at or before itself that are no
+ * more than `left` behind it or among the first `sinks` (left < 0: all of them).  A row with
+ * L - Sq + i < 0 sees no key: out = 0, lse = -inf.
+ * q : [B][Sq][H][D], k_cache and v_cache : [B][S_max][Hkv][D]; strides, kv_len, out, lse, types
+ *   and limits as cpattn_window_fwd.  The lengths are read on the device, so a captured call
+ *   follows a sequence as it grows.
+ * Errors: as cpattn_window_fwd (S_max >= 1).
+ */
+CPATTN_API int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache,
+                                    const int* kv_len, void* out, float* lse, int B, int H, int Hkv,
+                                    int Sq, int S_max, int D, long long q_stride, long long k_stride,
+                                    long long v_stride, float scale, int left, int sinks,
+                                    int in_dtype, int out_dtype, cpattn_stream_t stream);
+
+/* How cpattn_rope_frequencies stretches a context. */
+typedef enum {
+  CPATTN_ROPE_PLAIN = 0,   /* base^(-2p/rot) */
+  CPATTN_ROPE_LINEAR = 1,  /* every frequency divided by `stretch` (position interpolation) */
+  CPATTN_ROPE_NTK = 2,     /* base times stretch^(rot/(rot-2)): the slowest pair is stretched
+                              by `stretch`, the fastest not at all */
+  CPATTN_ROPE_BY_PARTS = 3 /* by the turns a pair makes over train_len positions: beta_fast or
+                              more unchanged, beta_slow or fewer divided by `stretch`, linear
+                              between; factor = 0.1 ln(stretch) + 1 */
+} cpattn_rope_scaling;
+
+/*
+ * cpattn_rope_frequencies -- radians per position of the rot/2 rotated pairs, in 64 bits, and
+ * the factor on the rotated part, into HOST memory (copy freq to the device for the calls
+ * below).  base > 1; stretch >= 1 except for CPATTN_ROPE_PLAIN; train_len > 0 and
+ * beta_fast > beta_slow > 0 for CPATTN_ROPE_BY_PARTS (0 < rot <= 256, even).  factor may be NULL.
+ * Errors: CPATTN_ERR_NULL, _SHAPE, _UNSUPPORTED.
+ */
+CPATTN_API int cpattn_rope_frequencies(double* freq, float* factor, int rot, double base, int scaling,
+                                       double stretch, double train_len, double beta_fast,
+                                       double beta_slow);
+
+/*
+ * cpattn_rope -- rotary positions.  Pair p of the first `rot` elements of every head row of
+ * token t turns by  angle = sum_{a < n_axes} pos[t % pos_rows][a] * freq[a][p] :
+ *   y_a = (x_a cos - x_b sin) * factor,  y_b = (x_b cos + x_a sin) * factor
+ * with (a, b) = (2p, 2p + 1) when `interleaved`, else (p, p + rot/2); elements rot..D-1 are
+ * copied.  The angle is formed in 64 bits and reduced to part of a turn; the rest is float32,
+ * rounded once.  Positions may be negative, and a call with the negated positions and factor 1
+ * undoes one.  Several axes (frame, row, column of a video token) each turn the pairs whose
+ * freq[a][p] is not 0.
+ * x, y : [tokens][H][D] in `dtype` (BF16 or F32), x_stride / y_stride elements between tokens
+ *   (0: packed, H*D); y may be x itself with the same stride, and must not overlap it otherwise.
+ * pos : [pos_rows][n_axes] int32, freq : [n_axes][rot/2] double, both in device memory; tokens a
+ *   multiple of pos_rows (a batch of sequences at the same positions gives pos_rows = their
+ *   length).  2 <= rot <= D <= 256, rot even; 1 <= n_axes <= 4; tokens >= 0 (0 is a no-op that
+ *   checks no pointer); tokens*H below 2^31 - 4096.
+ * Errors: CPATTN_ERR_NULL, _SHAPE, _ALIGN (x, y 16 bytes; pos 4; freq 8), _UNSUPPORTED, _CUDA.
+ */
+CPATTN_API int cpattn_rope(const void* x, void* y, const int* pos, const double* freq, int tokens,
+                           int pos_rows, int H, int D, int rot, int n_axes, int interleaved,
+                           float factor, long long x_stride, long long y_stride, int dtype,
+                           cpattn_stream_t stream);
+
+/*
+ * cpattn_qk_norm_rope -- cpattn_rmsnorm of every query head row (weights gamma_q) and key head
+ * row (gamma_k), then cpattn_rope of both, in one pass with one rounding at the end:
+ *   n = ((x * r) * gamma) * out_scale,  r = 1 / sqrt(mean(x^2) + eps);  y = rotate(n).
+ * q : [tokens][Hq][D], k : [tokens][Hk][D]; strides, positions and limits as cpattn_rope, with
+ * tokens*(Hq + Hk) below 2^31 - 4096.  q and k may be heads of one wider row (a fused
+ * projection's output), also in place.  gamma_q, gamma_k : D float32, 16-byte aligned.
+ * Errors: as cpattn_rope.
+ */
+CPATTN_API int cpattn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                                   const float* gamma_q, const float* gamma_k, const int* pos,
+                                   const double* freq, int tokens, int pos_rows, int Hq, int Hk, int D,
+                                   int rot, int n_axes, int interleaved, float eps, float out_scale,
+                                   float factor, long long q_stride, long long k_stride,
+                                   long long q_out_stride, long long k_out_stride, int dtype,
+                                   cpattn_stream_t stream);
+
+/*
+ * cpattn_seq2head_qkv_norm_rope -- cpattn_seq2head_qkv_norm with the rotation of cpattn_rope
+ * applied to the normalised Q and K head rows on the way; V is copied unchanged.  Token
+ * r*S_local + s of the full sequence takes row r*S_local + s of pos ([P*S_local][n_axes]).
+ * gamma_q and gamma_k both NULL: rotation only (eps and out_scale unused).  bf16, D <= 256; other
+ * requirements as cpattn_seq2head_qkv and cpattn_rope.  No destination may overlap an input or
+ * another destination.
+ * Errors: CPATTN_ERR_NULL, _SHAPE, _ALIGN, _CUDA.
+ */
+CPATTN_API int cpattn_seq2head_qkv_norm_rope(const void* q, const void* k, const void* v, void* qh,
+                                             void* kh, void* vh, const float* gamma_q,
+                                             const float* gamma_k, const int* pos, const double* freq,
+                                             int P, int S_local, int H, int D, int rot, int n_axes,
+                                             int interleaved, float eps, float out_scale,
+                                             float factor, cpattn_stream_t stream);
+
 /* Human-readable name of a cpattn_status value (static string, never NULL). */
 CPATTN_API const char* cpattn_status_str(int status);
 
