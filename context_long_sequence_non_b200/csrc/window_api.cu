@@ -45,6 +45,10 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
   if (c->q_stride < q_row || c->k_stride < kv_row || c->v_stride < kv_row || c->q_stride > most ||
       c->k_stride > most || c->v_stride > most)
     return CPATTN_ERR_SHAPE;
+  // batches are less than 2^40 bytes apart (a tensor map's limit)
+  if (c->B > 1 && (c->Sq * c->q_stride * es >> 40 || c->Skv * c->k_stride * es >> 40 ||
+                   c->Skv * c->v_stride * es >> 40))
+    return CPATTN_ERR_SHAPE;
   if (c->q == nullptr || c->out == nullptr || (c->accumulate && c->lse == nullptr)) return CPATTN_ERR_NULL;
   if (c->Skv > 0 && (c->k == nullptr || c->v == nullptr)) return CPATTN_ERR_NULL;
   if (!aligned(c->q, 16) || !aligned(c->out, 16) || (c->lse != nullptr && !aligned(c->lse, 4)) ||
@@ -94,7 +98,14 @@ int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   const bool none = Skv == 0 || (c.right >= 0 && last + c.right < 0) ||
                     (c.left >= 0 && c.sinks == 0 && c.off - c.left >= Skv);
   if (c.accumulate && none) return CPATTN_OK;
-  return cuda_status(cpattn::launch_window_rows(c, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (c.in_f32) return cuda_status(cpattn::launch_window_rows(c, cs));
+  if (Skv == 0)
+    return cuda_status(cpattn::launch_fill_empty(out, size_t(B) * Sq * H * D * elem_size(out_dtype), lse,
+                                                 size_t(B) * H * Sq, cs));
+  int* err = cpattn::device_error_word();
+  if (err == nullptr) return CPATTN_ERR_CUDA;
+  return cuda_status(cpattn::launch_window_sm100(c, err, cs));
 }
 
 int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache, const int* kv_len,

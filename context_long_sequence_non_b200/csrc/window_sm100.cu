@@ -1,0 +1,576 @@
+// window_sm100.cu -- windowed attention on B200 tensor cores (tcgen05 + TMEM + TMA), bf16 in.
+//
+// For every (b, h, query row i) at position p the softmax runs over the keys of two ranges, the
+// early (sink) keys [0, early) and the window [lo, hi) (window.h), streamed over 128-key blocks:
+//   S = Q K^T,  x = S scale log2(e),  m' = max(m, x),  O' = O 2^(m - m') + 2^(x - m') V,
+// with the same base-2 online softmax and reference-max rule as attn_sm100.cu: a row's reference
+// moves only when a key above it could carry 1/kMinorWeightInv of the row or exceeds it by
+// rescale_log2, so that most blocks rescale nothing.
+//
+// One CTA takes 128 query rows of one (b, h) and two CTAs share an SM.  Windows are short -- ten
+// to forty blocks -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue would
+// be a large share of its life if nothing ran beside them; with two independent CTAs one's
+// softmax, start and end overlap the other's matrix products, and a tile visits its own key
+// blocks and no neighbour's.  The price, K and V not shared between two query tiles, is L2
+// traffic of 64 KB per 128 x 128 block, under half of what L2 delivers.
+//   warps 0-3  softmax, one thread per query row = TMEM lane
+//   warp  4    TMA producer: Q, then per block K (one ring) and V in two 64-key halves (another)
+//   warp  5    TMEM allocator; clears V rows that no row of the tile sees (below); one of its
+//              threads issues every tcgen05.mma
+// TMEM (256 columns): S (128 fp32; P written back over it as bf16 pairs) | O (D fp32).
+//
+// Hidden keys.  A block is masked per element only where some row of the warp does not see all
+// of it.  A hidden key's weight is exactly 0 or, on the polynomial's clamp, at most 2^-125 of a
+// weight of 1; 0 x NaN is NaN, though, so V rows that no row of the tile sees (past a
+// sequence's length, outside the window) are cleared in shared memory before the product.
+// Every wait is bounded (mbar_wait): a stalled pipeline sets the device error word and the CTA
+// drains and exits.
+#include <cuda_runtime.h>
+
+#include "api_common.h"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+#include "window.h"
+
+namespace cpattn {
+namespace {
+
+constexpr int kBlockM = 128;
+constexpr int kBlockN = 128;
+// Six warps: two CTAs per SM then have 168 registers a thread, which holds a row's 128 logits
+// (a 224-thread CTA would have 144, a 256-thread one 128).
+constexpr int kThreads = 192;
+constexpr int kWarpProducer = 4, kWarpMma = 5;
+constexpr uint32_t kTmemCols = 256;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kPolyPairs = 2;        // of every 8 pairs of exponentials, on the FMA pipe
+constexpr int kMinorWeightInv = 8;   // see attn_sm100.cu
+constexpr int kHalf = kBlockN / 2;   // keys of a V half and of a P handoff
+constexpr int kHalfPairs = kHalf / 2;
+
+template <int D>
+struct Geometry {
+  static constexpr int kBoxes = D / 64;                 // 64-column (128-byte) boxes per row
+  static constexpr int kBoxBytes = kBlockN * 128;       // a box of 128 rows
+  static constexpr int kVBoxBytes = kHalf * 128;        // a box of 64 rows
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kVBytes = kBoxes * kVBoxBytes;
+  // K blocks and V halves in flight: what two CTAs per SM leave room for
+  static constexpr int kK = D == 128 ? 1 : 2;
+  static constexpr int kV = D == 128 ? 3 : 4;
+  static constexpr int kOffK = kTileBytes;
+  static constexpr int kOffV = kOffK + kK * kTileBytes;
+  static constexpr int kOffBars = kOffV + kV * kVBytes;
+  static constexpr int kSmem = kOffBars + 256;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct __align__(8) Barriers {
+  uint64_t q_full, s_full, o_full, drain;
+  uint64_t p_part[2];  // P of keys 0..63 / 64..127 stored (the first: O rescaled too)
+  uint64_t k_full[2], k_empty[2];
+  uint64_t v_full[4], v_empty[4];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Barriers) <= 256, "barrier block");
+
+// 2^t for a pair of t <= 8 on the FMA pipe: Cody-Waite reduction and a degree-4 polynomial with
+// constant term 1 (gen_exp2_poly.py 4, max relative error 2.9e-6 in fp32: a quarter of the
+// weights carry it, and LSE in fp32 keeps six digits).  Clamped at -125.
+__device__ __forceinline__ float2 exp2_poly4(float2 t) {
+  constexpr float kShift = 12582912.0f;
+  constexpr float kC1 = 0.693124115f, kC2 = 0.240241066f, kC3 = 0.0559068285f, kC4 = 0.00958257634f;
+  t.x = fmaxf(t.x, -125.0f);
+  t.y = fmaxf(t.y, -125.0f);
+  const float2 j = fadd2(t, make_float2(kShift, kShift));
+  const float2 n = fadd2(j, make_float2(-kShift, -kShift));
+  const float2 f = fsub2(t, n);
+  float2 p = ffma2(f, make_float2(kC4, kC4), make_float2(kC3, kC3));
+  p = ffma2(p, f, make_float2(kC2, kC2));
+  p = ffma2(p, f, make_float2(kC1, kC1));
+  p = ffma2(p, f, make_float2(1.0f, 1.0f));
+  const uint32_t ex = __float_as_uint(j.x) << 23, ey = __float_as_uint(j.y) << 23;
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + ex),
+                     __uint_as_float(__float_as_uint(p.y) + ey));
+}
+
+// The key blocks of one tile: n_early blocks from key 0, then blocks from key w0.
+struct Blocks {
+  int early, lo, hi;  // keys that some row of the tile sees: [0, early) and [lo, hi)
+  int n_early, w0, n;
+  __device__ __forceinline__ int base(int j) const {
+    return j < n_early ? j * kBlockN : w0 + (j - n_early) * kBlockN;
+  }
+  // does some row of the tile see every key of [k0, k1)?
+  __device__ __forceinline__ bool all_seen(int k0, int k1) const {
+    return k1 <= early || (k0 >= lo && k1 <= hi);
+  }
+};
+
+__device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, int p_last, int len) {
+  const KeyRange a = visible_keys(p_first, c.left, c.right, c.sinks, len);
+  const KeyRange z = visible_keys(p_last, c.left, c.right, c.sinks, len);
+  Blocks t;
+  t.hi = z.hi;
+  t.lo = a.lo < t.hi ? a.lo : t.hi;
+  t.early = c.sinks < t.hi ? c.sinks : t.hi;
+  if (t.early >= t.lo) t.early = 0, t.lo = 0;  // one range
+  t.n_early = (t.early + kBlockN - 1) / kBlockN;
+  t.w0 = t.lo > t.n_early * kBlockN ? t.lo : t.n_early * kBlockN;
+  t.n = t.n_early + (t.hi > t.w0 ? (t.hi - t.w0 + kBlockN - 1) / kBlockN : 0);
+  return t;
+}
+
+// the low n bits, n clamped to 0..32
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <int D, bool kOutF32, bool kAcc>
+__global__ void __launch_bounds__(kThreads, 2)
+    window_sm100_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowCall c,
+                        int n_tiles, float scale_log2, float rescale_log2, int* err,
+                        long long wait_limit) {
+  using G = Geometry<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Barriers& bars = *reinterpret_cast<Barriers*>(smem + G::kOffBars);
+  const uint32_t smem_base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // CTAs run in index order, so the tiles with the most keys (the last ones, when the window
+  // grows with the position) come first within each head and the grid ends on short ones
+  const int tile = n_tiles - 1 - int(blockIdx.x % unsigned(n_tiles));
+  const int bh = int(blockIdx.x / unsigned(n_tiles));
+  const int b = bh / c.H, h = bh - b * c.H;
+  const int kvh = h / (c.H / c.Hkv);
+  const int q_first = tile * kBlockM;
+  volatile int* abort_flag = &bars.abort;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars.q_full), 1);
+    mbar_init(smem_u32(&bars.s_full), 1);
+    mbar_init(smem_u32(&bars.o_full), 1);
+    mbar_init(smem_u32(&bars.drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.p_part[i]), 4);  // one arrive per softmax warp
+      mbar_init(smem_u32(&bars.k_full[i]), 1);
+      mbar_init(smem_u32(&bars.k_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bars.v_full[i]), 1);
+      mbar_init(smem_u32(&bars.v_empty[i]), 1);
+    }
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  griddep_wait();
+  griddep_release();
+
+  const int len = sequence_length(c, b);
+  const int off = c.from_end ? len - c.Sq : c.off;
+  const int last_row = min(q_first + kBlockM, c.Sq) - 1;
+  const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len);
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ softmax warps
+    const int row = warp * 32 + lane;
+    const uint32_t lane_bits = uint32_t(warp * 32) << 16;
+    const uint32_t t_s = tmem + lane_bits;
+    const uint32_t t_o = tmem + lane_bits + kBlockN;
+    const uint32_t bar_s = smem_u32(&bars.s_full);
+    const uint32_t bar_p0 = smem_u32(&bars.p_part[0]);
+    const int q = q_first + row;
+    const bool in_range = q < c.Sq;
+    const KeyRange r = visible_keys(off + min(q, c.Sq - 1), c.left, c.right, c.sinks, len);
+    float m = -INFINITY;  // reference of x = s * scale * log2(e); -inf: no visible key so far
+    float l = 0.f;        // running sum of 2^(x - m)
+    bool ok = true;
+
+    for (int j = 0; j < blk.n; ++j) {
+      ok = mbar_wait(bar_s, j & 1, abort_flag, err, wait_limit);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      float x[kBlockN];
+      {
+        uint32_t t[kBlockN];
+        tmem_ld128(t_s, t);
+#pragma unroll
+        for (int e = 0; e < kBlockN; ++e) x[e] = __uint_as_float(t[e]);
+      }
+      const int kb = blk.base(j);
+      const bool sees_all = (kb >= r.lo && kb + kBlockN <= r.hi) || kb + kBlockN <= r.early;
+      if (!__all_sync(0xffffffffu, sees_all)) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int k0 = kb + 32 * w;
+          const uint32_t see = (low_bits(r.hi - k0) & ~low_bits(r.lo - k0)) | low_bits(r.early - k0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(see & (1u << e))) x[32 * w + e] = -INFINITY;
+        }
+      }
+      float mx;
+      {
+        float l1[44];
+#pragma unroll
+        for (int i = 0; i < 42; ++i) l1[i] = max3(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+        l1[42] = x[126];
+        l1[43] = x[127];
+        float l2[16];
+#pragma unroll
+        for (int i = 0; i < 14; ++i) l2[i] = max3(l1[3 * i], l1[3 * i + 1], l1[3 * i + 2]);
+        l2[14] = l1[42];
+        l2[15] = l1[43];
+        float l3[6];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) l3[i] = max3(l2[3 * i], l2[3 * i + 1], l2[3 * i + 2]);
+        l3[5] = l2[15];
+        mx = fmaxf(max3(l3[0], l3[1], l3[2]), max3(l3[3], l3[4], l3[5]));
+      }
+      const float m_tile = mx * scale_log2;
+      float alpha = 1.0f;
+      bool rescale = false;
+      if (j == 0) {
+        m = m_tile;
+      } else {
+        // a row that has seen no key yet (m = -inf) takes the block's maximum; its O is 0
+        const float d = m_tile - m;
+        bool grow = d > rescale_log2;
+        if (!grow && d > 0.f) grow = ex2(d) * float(kMinorWeightInv - 1) >= l;
+        rescale = __any_sync(0xffffffffu, grow);
+        if (rescale) {
+          alpha = grow ? ex2(m - m_tile) : 1.0f;
+          if (grow) m = m_tile;
+          l *= alpha;
+        }
+      }
+      const float neg_m = m == -INFINITY ? 0.f : -m;
+      const float2 sl2 = make_float2(scale_log2, scale_log2);
+      const float2 nm2 = make_float2(neg_m, neg_m);
+      float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        uint32_t pk[kHalfPairs];
+#pragma unroll
+        for (int e = 0; e < kHalfPairs; ++e) {
+          const int cc = 2 * (part * kHalfPairs + e);
+          const float2 t = ffma2(make_float2(x[cc], x[cc + 1]), sl2, nm2);
+          float2 pv;
+          if ((e & 7) >= 8 - kPolyPairs) {
+            pv = exp2_poly4(t);
+          } else {
+            pv.x = ex2(t.x);
+            pv.y = ex2(t.y);
+          }
+          if (e & 1) acc1 = fadd2(acc1, pv);
+          else acc0 = fadd2(acc0, pv);
+          pk[e] = pack_bf16x2(pv.x, pv.y);  // weights in bf16 for the product; l keeps fp32
+        }
+        tmem_st_any(t_s + part * kHalfPairs, pk);
+        if (part == 0 && rescale) {
+          const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+          for (int oc = 0; oc < D / 32; ++oc) {
+            uint32_t t[32];
+            tmem_ld32(t_o + oc * 32, t);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 o = fmul2(make_float2(__uint_as_float(t[e]), __uint_as_float(t[e + 1])), a2);
+              t[e] = __float_as_uint(o.x);
+              t[e + 1] = __float_as_uint(o.y);
+            }
+            tmem_st32(t_o + oc * 32, t);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p0 + 8 * part);
+      }
+      const float2 acc = fadd2(acc0, acc1);
+      l += acc.x + acc.y;
+    }
+
+    // ------------------------------------------------------------------ epilogue
+    const int qr = in_range ? q : 0;
+    const size_t row_off = ((size_t(b) * c.Sq + qr) * c.H + h) * size_t(D);
+    const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + qr;
+    if (ok && blk.n > 0) {
+      ok = mbar_wait(smem_u32(&bars.o_full), 0, abort_flag, err, wait_limit);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (ok) {
+      tc_fence_after();
+      const bool empty = m == -INFINITY;
+      const float lc2 = m + log2f(l);
+      float fa = 0.f, fc = empty ? 0.f : 1.0f / l;
+      float lse_out = empty ? -INFINITY : lc2 * kLn2;
+      bool write = in_range;
+      if constexpr (kAcc) {
+        if (empty) write = false;  // nothing to add: the running row stays as it is
+        if (write) {
+          const float la2 = c.lse[lse_idx] * kLog2e;
+          const float mx = fmaxf(la2, lc2);
+          const float wa = exp2f(la2 - mx), wc = exp2f(lc2 - mx);
+          const float tot = wa + wc;
+          fa = wa / tot;
+          fc = wc / (tot * l);
+          lse_out = (mx + log2f(tot)) * kLn2;
+        }
+      }
+#pragma unroll 1
+      for (int oc = 0; oc < D / 32; ++oc) {
+        uint32_t t[32];
+        __syncwarp();
+        if (blk.n > 0) tmem_ld32(t_o + oc * 32, t);
+        if (!write) continue;
+        if (empty) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t[e] = 0u;
+        }
+        if constexpr (kOutF32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(c.out) + row_off + oc * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float4 v = make_float4(__uint_as_float(t[4 * e]) * fc, __uint_as_float(t[4 * e + 1]) * fc,
+                                   __uint_as_float(t[4 * e + 2]) * fc, __uint_as_float(t[4 * e + 3]) * fc);
+            if (kAcc && fa != 0.f) {  // an empty accumulator row is never read
+              const float4 a = dst[e];
+              v.x = fmaf(fa, a.x, v.x);
+              v.y = fmaf(fa, a.y, v.y);
+              v.z = fmaf(fa, a.z, v.z);
+              v.w = fmaf(fa, a.w, v.w);
+            }
+            dst[e] = v;
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + row_off + oc * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(t[8 * e + i]) * fc;
+            if (kAcc && fa != 0.f) {
+              const uint4 a = dst[e];
+              const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[2 * i] = fmaf(fa, __uint_as_float(aw[i] << 16), o[2 * i]);
+                o[2 * i + 1] = fmaf(fa, __uint_as_float(aw[i] & 0xFFFF0000u), o[2 * i + 1]);
+              }
+            }
+            uint4 v;
+            v.x = pack_bf16x2(o[0], o[1]);
+            v.y = pack_bf16x2(o[2], o[3]);
+            v.z = pack_bf16x2(o[4], o[5]);
+            v.w = pack_bf16x2(o[6], o[7]);
+            dst[e] = v;
+          }
+        }
+      }
+      if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
+    }
+  } else if (warp == kWarpProducer) {
+    // ------------------------------------------------------------------ TMA producer
+    if (blk.n > 0 && elect_one()) {
+      const uint32_t bar_q = smem_u32(&bars.q_full);
+      mbar_arrive_expect_tx(bar_q, G::kTileBytes);
+#pragma unroll
+      for (int bx = 0; bx < G::kBoxes; ++bx)
+        tma_load_4d(smem_base + bx * G::kBoxBytes, &tm_q, bar_q, bx * 64, h, q_first, b);
+      int k_issued = 0, v_issued = 0;
+      bool go = true;
+      for (int j = 0; go && j < blk.n; ++j) {
+        const int kb = blk.base(j);
+        const int ks = j % G::kK;
+        if (!mbar_wait(smem_u32(&bars.k_empty[ks]), (uint32_t(j / G::kK) & 1u) ^ 1u, abort_flag, err,
+                       wait_limit))
+          break;
+        const uint32_t bar_k = smem_u32(&bars.k_full[ks]);
+        mbar_arrive_expect_tx(bar_k, G::kTileBytes);
+#pragma unroll
+        for (int bx = 0; bx < G::kBoxes; ++bx)
+          tma_load_4d(smem_base + G::kOffK + ks * G::kTileBytes + bx * G::kBoxBytes, &tm_k, bar_k, bx * 64,
+                      kvh, kb, b);
+        k_issued = j + 1;
+        for (int half = 0; half < 2; ++half) {
+          const int use = 2 * j + half, vs = use % G::kV;
+          if (!mbar_wait(smem_u32(&bars.v_empty[vs]), (uint32_t(use / G::kV) & 1u) ^ 1u, abort_flag, err,
+                         wait_limit)) {
+            go = false;
+            break;
+          }
+          const uint32_t bar_v = smem_u32(&bars.v_full[vs]);
+          mbar_arrive_expect_tx(bar_v, G::kVBytes);
+#pragma unroll
+          for (int bx = 0; bx < G::kBoxes; ++bx)
+            tma_load_4d(smem_base + G::kOffV + vs * G::kVBytes + bx * G::kVBoxBytes, &tm_v, bar_v, bx * 64,
+                        kvh, kb + half * kHalf, b);
+          v_issued = use + 1;
+        }
+      }
+      // every issued copy lands before the CTA's shared memory is released
+      drain_wait(bar_q, 0, wait_limit);
+      for (int j = k_issued > G::kK ? k_issued - G::kK : 0; j < k_issued; ++j)
+        drain_wait(smem_u32(&bars.k_full[j % G::kK]), uint32_t(j / G::kK) & 1u, wait_limit);
+      for (int u = v_issued > G::kV ? v_issued - G::kV : 0; u < v_issued; ++u)
+        drain_wait(smem_u32(&bars.v_full[u % G::kV]), uint32_t(u / G::kV) & 1u, wait_limit);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------------ MMA issuer
+    // the whole warp walks the loop (it clears hidden V rows together); `leader` issues
+    if (blk.n > 0) {
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, true);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, err, wait_limit)));
+      };
+      // S = Q K^T over D in K = 16 steps: 32 bytes per step inside a 128-byte swizzled row, the
+      // next 64 columns in the next box
+      auto issue_qk = [&](int ks) {
+        if (!leader) return;
+        const uint32_t k_addr = smem_base + G::kOffK + ks * G::kTileBytes;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * G::kBoxBytes + (kk & 3) * 32;
+          mma_ss(tmem, sdesc_sw128(smem_base + o, 16, 1024), sdesc_sw128(k_addr + o, 16, 1024), idesc_qk,
+                 kk > 0 ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&bars.s_full));
+        tc_commit(smem_u32(&bars.k_empty[ks]));
+      };
+      bool ok = wait(&bars.q_full, 0) && wait(&bars.k_full[0], 0);
+      if (ok) issue_qk(0);
+      for (int j = 0; ok && j < blk.n; ++j) {
+        const int kb = blk.base(j);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int use = 2 * j + half, vs = use % G::kV;
+          const uint32_t v_off = G::kOffV + vs * G::kVBytes;
+          ok = ok && wait(&bars.v_full[vs], uint32_t(use / G::kV) & 1u);
+          const int k0 = kb + half * kHalf, k1 = min(k0 + kHalf, c.Skv);  // rows past Skv arrive as 0
+          if (ok && k0 < k1 && !blk.all_seen(k0, k1)) {
+            for (int rr = lane >> 3; rr < k1 - k0; rr += 4) {
+              const int key = k0 + rr;
+              if (key < blk.early || (key >= blk.lo && key < blk.hi)) continue;
+#pragma unroll
+              for (int bx = 0; bx < G::kBoxes; ++bx)  // a whole 128-byte row: any swizzle
+                *reinterpret_cast<uint4*>(smem + v_off + bx * G::kVBoxBytes + rr * 128 + (lane & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // the tensor core reads the zeros
+            __syncwarp();
+          }
+          ok = ok && wait(&bars.p_part[half], uint32_t(j) & 1u);
+          if (!ok) break;
+          // O += P V over 64 keys in K = 16 steps: P from TMEM (8 columns per step), V MN-major
+          // (16 key rows = 2 KB per step, the next 64 columns of D in the next box)
+          if (leader) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              mma_ts(tmem + kBlockN, tmem + half * kHalfPairs + kk * 8,
+                     sdesc_sw128(smem_base + v_off + kk * 16 * 128, G::kVBoxBytes, 1024), idesc_pv,
+                     (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&bars.v_empty[vs]));
+          }
+        }
+        if (!ok) break;
+        if (j + 1 < blk.n) {
+          const int ks = (j + 1) % G::kK;
+          ok = wait(&bars.k_full[ks], uint32_t((j + 1) / G::kK) & 1u);
+          if (ok) issue_qk(ks);
+        }
+      }
+      if (leader) {
+        if (ok) tc_commit(smem_u32(&bars.o_full));
+        tc_commit(smem_u32(&bars.drain));  // no MMA may still be writing TMEM when it is freed
+        drain_wait(smem_u32(&bars.drain), 0, wait_limit);
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// [B][S][H][D] bf16 tensor whose tokens are `stride` elements apart: 64 columns x 1 head x
+// `rows` tokens x 1 batch, 128-byte swizzle; rows past S read as 0.
+bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long long stride, unsigned rows) {
+  auto fn = tensor_map_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(S), cuuint64_t(B)};
+  const cuuint64_t token = cuuint64_t(stride) * 2;
+  const cuuint64_t strides[3] = {cuuint64_t(D) * 2, token, B > 1 ? token * cuuint64_t(S) : token};
+  const cuuint32_t box[4] = {64, 1, rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kOutF32, bool kAcc>
+cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   int* err, cudaStream_t stream) {
+  auto kernel = window_sm100_kernel<D, kOutF32, kAcc>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geometry<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int n_tiles = (c.Sq + kBlockM - 1) / kBlockM;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(n_tiles) * c.H * c.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Geometry<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, n_tiles, float(double(c.scale) * 1.4426950408889634074),
+                            kRescaleLog2, err, kDefaultWaitLimit);
+}
+
+template <int D>
+cudaError_t launch_d(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     int* err, cudaStream_t stream) {
+  if (c.out_f32)
+    return c.accumulate ? launch<D, true, true>(c, tq, tk, tv, err, stream)
+                        : launch<D, true, false>(c, tq, tk, tv, err, stream);
+  return c.accumulate ? launch<D, false, true>(c, tq, tk, tv, err, stream)
+                      : launch<D, false, false>(c, tq, tk, tv, err, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM) ||
+      !encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
+      !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kHalf))
+    return cudaErrorInvalidValue;
+  return c.D == 128 ? launch_d<128>(c, tq, tk, tv, err, stream) : launch_d<64>(c, tq, tk, tv, err, stream);
+}
+
+}  // namespace cpattn
