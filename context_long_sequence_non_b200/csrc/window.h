@@ -53,4 +53,7 @@ cudaError_t launch_window_rows(const WindowCall& c, cudaStream_t stream);
 // Tensor-core kernel: bf16 inputs, D 64 or 128, Skv >= 1.
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream);
 
+// Single-token form (from_end, right = 0): bf16 inputs, D 64 or 128.
+cudaError_t launch_window_decode(const WindowCall& c, cudaStream_t stream);
+
 }  // namespace cpattn

@@ -118,7 +118,8 @@ int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache
   if (st != CPATTN_OK) return st;
   if (S_max < 1) return CPATTN_ERR_SHAPE;
   if (sinks > S_max) c.sinks = S_max;
-  return cuda_status(cpattn::launch_window_rows(c, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(c.in_f32 ? cpattn::launch_window_rows(c, cs) : cpattn::launch_window_decode(c, cs));
 }
 
 }  // extern "C"
