@@ -6,8 +6,15 @@
 // first normalised: x * r * gamma * out_scale, r = 1 / sqrt(mean(x^2) + eps).  All in fp32,
 // rounded once when stored.  The angle sum_a pos_a * freq_a is formed in 64 bits and reduced to
 // a fraction of a turn before the fp32 sine and cosine: at position 10^6 a fp32 angle has lost
-// all but a few bits of its fraction.  A block takes a few tokens, computes their cos/sin once
-// into shared memory, and its warps then take the (token, head) rows.
+// all but a few bits of its fraction.
+//
+// One pass over the heads; HBM bounds it.  rope_kernel is the form for head rows of whole
+// 16-byte vectors (D and rot multiples of 16, 16-byte spacing): a warp takes one token, computes
+// the token's cos/sin once, and every lane keeps the 8 pairs it needs of them -- the same ones
+// for every head -- in registers while it streams the token's heads, 16 elements a lane.  A lane
+// holds both elements of its pairs in either layout, so the rotation needs no exchange; the norm
+// is one shuffle reduction over a row's lanes.  rope_rows_kernel takes everything else, an element
+// at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,6 +23,7 @@
 #include "kernels.h"
 #include "norm_math.cuh"
 #include "rope.h"
+#include "sm100_ptx.cuh"
 
 namespace cpattn {
 namespace {
@@ -39,7 +47,9 @@ __device__ __forceinline__ float2 pair_angle(const RopeCall& c, int pr, int p) {
   return make_float2(co * c.factor, s * c.factor);
 }
 
-// One warp per head row, one element at a time: any D <= 256 and any even rot <= D.
+// One warp per head row, one element at a time: any D <= 256 and any even rot <= D.  A block
+// takes a few tokens, computes their cos/sin once into shared memory, and its warps take the
+// (token, head) rows.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeCall c, int block_tokens) {
   extern __shared__ float2 cs[];  // [block_tokens][rot / 2]
@@ -106,9 +116,219 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeCall c, i
   }
 }
 
+// ------------------------------------------------------------------ vector form
+constexpr int kWarpsPerBlock = kThreads / 32;
+
+// 8 consecutive elements of a row.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // bf16 -> fp32 is exact
+      f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+    v = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                   pack_bf16x2(f[3].x, f[3].y));
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+    a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  }
+};
+
+// A warp takes (token, part): part `p` of `parts` of the token's heads.  A row's D/16 lanes (padded
+// to `lanes`, a power of two) hold two 8-element vectors each: lane l < rot/16 the vectors l and
+// l + rot/16 of the rotated elements, the others two of the rest.
+template <typename T, bool kInterleaved, int kUnroll>
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeCall c, int lanes_log2,
+                                                           int parts) {
+  __shared__ __align__(16) float2 cs_sh[kWarpsPerBlock][kRopeMaxD / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2* cs = cs_sh[warp];
+  const int D = c.D, half = c.rot / 2;
+  const int L = D / 16, nr = c.rot / 16;
+  const int rows_per_warp = 32 >> lanes_log2;
+  const int l = lane & ((1 << lanes_log2) - 1), sub = lane >> lanes_log2;
+  const bool live = l < L, turns = l < nr;
+  const int va = 8 * (turns ? l : l + nr);                 // element of the first vector
+  const int vb = turns ? va + half : va + 8 * (L - nr);    // and of the second
+  const float inv_d = 1.0f / float(D);
+
+  griddep_wait();
+  griddep_release();
+
+  // weights of the normalised tensors (at most the first two) at this lane's elements
+  float2 ga[2][4], gb[2][4];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const bool have = t < c.n_tensors && c.t[t].gamma != nullptr && live;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ga[t][i] = have ? *reinterpret_cast<const float2*>(c.t[t].gamma + va + 2 * i) : make_float2(0.f, 0.f);
+      gb[t][i] = have ? *reinterpret_cast<const float2*>(c.t[t].gamma + vb + 2 * i) : make_float2(0.f, 0.f);
+    }
+  }
+
+  const long long n_items = (long long)c.tokens * parts;
+  const long long n_warps = (long long)gridDim.x * kWarpsPerBlock;
+  for (long long item = (long long)blockIdx.x * kWarpsPerBlock + warp; item < n_items; item += n_warps) {
+    const int token = int(item / parts), part = int(item - (long long)token * parts);
+    const int pr = token % c.pos_rows;
+    __syncwarp();  // the previous token's angles are read no more
+    for (int p = lane; p < half; p += 32) cs[p] = pair_angle(c, pr, p);
+    __syncwarp();
+    // cos and sin of this lane's pairs: 8 l + i (halves), or 4 (va / 8) + i and 4 (vb / 8) + i
+    float2 w[8];
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = cs[kInterleaved ? (i < 4 ? va / 2 + i : vb / 2 + i - 4) : va + i];
+    }
+#pragma unroll
+    for (int ti = 0; ti < 3; ++ti) {
+      if (ti >= c.n_tensors) break;
+      const RopeTensor& t = c.t[ti];
+      const T* src = static_cast<const T*>(t.src) + (long long)token * t.src_stride;
+      T* dst = static_cast<T*>(t.dst) + (long long)token * t.dst_stride;
+      const int h_begin = int((long long)t.heads * part / parts), h_end = int((long long)t.heads * (part + 1) / parts);
+      for (int h0 = h_begin; h0 < h_end; h0 += rows_per_warp * kUnroll) {
+        Vec8<T> xa[kUnroll], xb[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int h = h0 + u * rows_per_warp + sub;
+          if (live && h < h_end) {
+            xa[u].load(src + (long long)h * D + va);
+            xb[u].load(src + (long long)h * D + vb);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (h0 + u * rows_per_warp >= h_end) break;  // the whole warp
+          const int h = h0 + u * rows_per_warp + sub;
+          const bool on = live && h < h_end;
+          if (ti < 2 && (t.gamma != nullptr || t.rotate)) {  // the third tensor only moves
+            float2 a[4], b[4];
+            xa[u].get(a);
+            xb[u].get(b);
+            if (t.gamma != nullptr) {
+              float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s2 = ffma2(b[i], b[i], ffma2(a[i], a[i], s2));
+              float ss = on ? s2.x + s2.y : 0.f;
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1)
+                if (o < (1 << lanes_log2)) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+              const float mean = ss * inv_d + c.eps;
+              const float r = mean > 0.f ? rsqrt_refined(mean) : 0.f;  // a zero row with eps = 0 stays 0
+              const float2 r2 = make_float2(r, r), os = make_float2(c.out_scale, c.out_scale);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[i] = fmul2(fmul2(fmul2(a[i], r2), ga[ti & 1][i]), os);
+                b[i] = fmul2(fmul2(fmul2(b[i], r2), gb[ti & 1][i]), os);
+              }
+            }
+            if (turns && t.rotate) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (kInterleaved) {  // (x0 c - x1 s, x1 c + x0 s)
+                  const float2 x = a[i], y = b[i], wa = w[i], wb = w[4 + i];
+                  a[i] = ffma2(x, make_float2(wa.x, wa.x), fmul2(make_float2(x.y, x.x), make_float2(-wa.y, wa.y)));
+                  b[i] = ffma2(y, make_float2(wb.x, wb.x), fmul2(make_float2(y.y, y.x), make_float2(-wb.y, wb.y)));
+                } else {  // pairs 2i and 2i + 1: a cos - b sin, b cos + a sin
+                  const float2 x = a[i], y = b[i];
+                  const float2 co = make_float2(w[2 * i].x, w[2 * i + 1].x);
+                  const float2 si = make_float2(w[2 * i].y, w[2 * i + 1].y);
+                  a[i] = ffma2(x, co, fmul2(y, make_float2(-si.x, -si.y)));
+                  b[i] = ffma2(y, co, fmul2(x, si));
+                }
+              }
+            }
+            xa[u].set(a);
+            xb[u].set(b);
+          }
+          if (on) {
+            const int g = t.group_magic == 0 ? h : int(__umulhi(unsigned(h), t.group_magic));  // h / group
+            T* d = dst + g * t.group_stride + (long long)(h - g * t.group) * D;
+            xa[u].store(d + va);
+            xb[u].store(d + vb);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_vector(const RopeCall& c, int max_heads, cudaStream_t stream) {
+  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+  int lanes_log2 = 0;
+  while ((1 << lanes_log2) < c.D / 16) ++lanes_log2;
+  const int rows_per_warp = 32 >> lanes_log2;
+  // few tokens: several warps share a token's heads (each with its own angles), down to one
+  // warp-load of heads each, until the GPU has a few warps per scheduler
+  const long long want = (long long)sm_count() * 16;
+  int parts = 1;
+  while (c.tokens * parts < want && parts * rows_per_warp < max_heads) parts *= 2;
+  const long long blocks = ((long long)c.tokens * parts + kWarpsPerBlock - 1) / kWarpsPerBlock;
+  const long long cap = (long long)sm_count() * 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, c.interleaved ? rope_kernel<T, true, kUnroll> : rope_kernel<T, false, kUnroll>, c,
+                            lanes_log2, parts);
+}
+
+// Can the vector form take this call?  Whole vectors, every row on 16 bytes.
+bool vector_form(const RopeCall& c) {
+  if (c.D % 16 != 0 || c.rot % 16 != 0) return false;
+  const int vec = c.f32 ? 4 : 8;
+  for (int i = 0; i < c.n_tensors; ++i)
+    if (c.t[i].src_stride % vec != 0 || c.t[i].dst_stride % vec != 0 || c.t[i].group_stride % vec != 0) return false;
+  return true;
+}
+
 }  // namespace
 
-cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeCall& call, cudaStream_t stream) {
+  RopeCall c = call;
+  int max_heads = 0;
+  for (int i = 0; i < c.n_tensors; ++i) {
+    RopeTensor& t = c.t[i];
+    // h / group = umulhi(h, ceil(2^32 / group)) for h, group < 2^16; group 1 has no 32-bit form
+    t.group_magic = t.group == 1 ? 0u : unsigned(((1ULL << 32) + t.group - 1) / t.group);
+    if (t.heads > max_heads) max_heads = t.heads;
+  }
+  if (vector_form(c))
+    return c.f32 ? launch_vector<float>(c, max_heads, stream) : launch_vector<__nv_bfloat16>(c, max_heads, stream);
   const int block_tokens = 4;
   const int tiles = (c.tokens + block_tokens - 1) / block_tokens;
   const int cap = sm_count() * 8;

@@ -17,6 +17,7 @@ struct RopeTensor {
   long long src_stride, dst_stride, group_stride;
   int heads, group;
   bool rotate;
+  unsigned group_magic;  // filled in by the launcher
 };
 
 // Up to three tensors of the same tokens.  The angle of pair p at token t is

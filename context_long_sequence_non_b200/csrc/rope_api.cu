@@ -132,7 +132,7 @@ int cpattn_rope(const void* x, void* y, const int* pos, const double* freq, int 
                 long long y_stride, int dtype, cpattn_stream_t stream) {
   RopeCall c{};
   c.n_tensors = 1;
-  c.t[0] = RopeTensor{x, y, nullptr, x_stride, y_stride, 0, H, H, true};
+  c.t[0] = RopeTensor{x, y, nullptr, x_stride, y_stride, 0, H, H, true, 0};
   c.pos = pos, c.freq = freq, c.tokens = tokens, c.pos_rows = pos_rows, c.D = D, c.rot = rot;
   c.n_axes = n_axes, c.interleaved = interleaved != 0, c.factor = factor, c.eps = 0.f, c.out_scale = 1.f;
   const int st = check(&c, dtype, false);
@@ -147,8 +147,8 @@ int cpattn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, 
                         cpattn_stream_t stream) {
   RopeCall c{};
   c.n_tensors = 2;
-  c.t[0] = RopeTensor{q, q_out, gamma_q, q_stride, q_out_stride, 0, Hq, Hq, true};
-  c.t[1] = RopeTensor{k, k_out, gamma_k, k_stride, k_out_stride, 0, Hk, Hk, true};
+  c.t[0] = RopeTensor{q, q_out, gamma_q, q_stride, q_out_stride, 0, Hq, Hq, true, 0};
+  c.t[1] = RopeTensor{k, k_out, gamma_k, k_stride, k_out_stride, 0, Hk, Hk, true, 0};
   c.pos = pos, c.freq = freq, c.tokens = tokens, c.pos_rows = pos_rows, c.D = D, c.rot = rot;
   c.n_axes = n_axes, c.interleaved = interleaved != 0, c.factor = factor, c.eps = eps, c.out_scale = out_scale;
   const int st = check(&c, dtype, false);
@@ -170,9 +170,9 @@ int cpattn_seq2head_qkv_norm_rope(const void* q, const void* k, const void* v, v
   const long long group = (long long)T * Hp * D, row = (long long)Hp * D;
   RopeCall c{};
   c.n_tensors = 3;
-  c.t[0] = RopeTensor{q, qh, gamma_q, 0, row, group, H, Hp, true};
-  c.t[1] = RopeTensor{k, kh, gamma_k, 0, row, group, H, Hp, true};
-  c.t[2] = RopeTensor{v, vh, nullptr, 0, row, group, H, Hp, false};
+  c.t[0] = RopeTensor{q, qh, gamma_q, 0, row, group, H, Hp, true, 0};
+  c.t[1] = RopeTensor{k, kh, gamma_k, 0, row, group, H, Hp, true, 0};
+  c.t[2] = RopeTensor{v, vh, nullptr, 0, row, group, H, Hp, false, 0};
   c.pos = pos, c.freq = freq, c.tokens = T, c.pos_rows = T, c.D = D, c.rot = rot;
   c.n_axes = n_axes, c.interleaved = interleaved != 0, c.factor = factor, c.eps = eps, c.out_scale = out_scale;
   const int st = check(&c, CPATTN_BF16, true);
