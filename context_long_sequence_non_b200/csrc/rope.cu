@@ -11,10 +11,14 @@
 // One pass over the heads; HBM bounds it.  rope_kernel is the form for head rows of whole
 // 16-byte vectors (D and rot multiples of 16, 16-byte spacing): a warp takes one token, computes
 // the token's cos/sin once, and every lane keeps the 8 pairs it needs of them -- the same ones
-// for every head -- in registers while it streams the token's heads, 16 elements a lane.  A lane
+// for every head -- in registers while the token's heads stream by, 16 elements a lane.  A lane
 // holds both elements of its pairs in either layout, so the rotation needs no exchange; the norm
-// is one shuffle reduction over a row's lanes.  rope_rows_kernel takes everything else, an element
-// at a time.
+// is one shuffle reduction over a row's lanes.  Loads run ahead through a small cp.async ring per
+// warp, across heads and tokens, so the angles' latency and the stores hide behind them (plain
+// register loads, four rows at a time, took 73 us where this takes 61).  Frequencies and weights
+// sit in shared memory.  Measured on a B200: 44160 tokens x 16 heads of 128, three axes, 61 us
+// (5.9 TB/s, 90% of the measured copy rate); norm + rotation + re-partition of Q, K and V of the
+// same size 180 us (6.0 TB/s, 92%).  rope_rows_kernel takes every other shape, an element at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,16 +39,21 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// (cos, sin) * factor of an angle in radians.
+__device__ __forceinline__ float2 turn_by(double angle, float factor) {
+  angle *= 0.15915494309189533577;  // 1 / (2 pi): whole turns drop out exactly
+  angle -= rint(angle);
+  float s, co;
+  sincospif(2.0f * float(angle), &s, &co);
+  return make_float2(co * factor, s * factor);
+}
+
 // (cos, sin) * factor of pair p at position row `pr`.
 __device__ __forceinline__ float2 pair_angle(const RopeCall& c, int pr, int p) {
-  double turn = 0.0;
+  double angle = 0.0;
   for (int a = 0; a < c.n_axes; ++a)
-    turn = fma(double(c.pos[(long long)pr * c.n_axes + a]), c.freq[(long long)a * (c.rot / 2) + p], turn);
-  turn *= 0.15915494309189533577;  // 1 / (2 pi)
-  turn -= rint(turn);
-  float s, co;
-  sincospif(2.0f * float(turn), &s, &co);
-  return make_float2(co * c.factor, s * c.factor);
+    angle = fma(double(c.pos[(long long)pr * c.n_axes + a]), c.freq[(long long)a * (c.rot / 2) + p], angle);
+  return turn_by(angle, c.factor);
 }
 
 // One warp per head row, one element at a time: any D <= 256 and any even rot <= D.  A block
@@ -118,14 +127,25 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeCall c, i
 
 // ------------------------------------------------------------------ vector form
 constexpr int kWarpsPerBlock = kThreads / 32;
+constexpr int kBlocksPerSm = 2;
 
-// 8 consecutive elements of a row.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 8 consecutive elements of a row, kSlots 16-byte slots each; a warp keeps kStages - 1 steps of loads
+// in flight (2 blocks x 8 warps x 3 KB per SM in bf16; 2 and 6 stages measured 222 and 202 us where
+// 4 take 180, on the 44160-token norm + re-partition of Q, K and V).  `fetch` copies them to this lane's 16-byte slots of a stage (32
+// lanes apart), `load` takes them from there.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
+  static constexpr int kSlots = 1;
+  static constexpr int kStages = 4;
   uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void fetch(uint32_t slot, const __nv_bfloat16* p) { cp_async16(slot, p); }
+  __device__ __forceinline__ void load(const uint8_t* slot) { v = *reinterpret_cast<const uint4*>(slot); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void get(float2 (&f)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -140,10 +160,16 @@ struct Vec8<__nv_bfloat16> {
 };
 template <>
 struct Vec8<float> {
+  static constexpr int kSlots = 2;
+  static constexpr int kStages = 3;
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+  static __device__ __forceinline__ void fetch(uint32_t slot, const float* p) {
+    cp_async16(slot, p);
+    cp_async16(slot + 512, p + 4);
+  }
+  __device__ __forceinline__ void load(const uint8_t* slot) {
+    a = *reinterpret_cast<const float4*>(slot);
+    b = *reinterpret_cast<const float4*>(slot + 512);
   }
   __device__ __forceinline__ void store(float* p) const {
     *reinterpret_cast<float4*>(p) = a;
@@ -162,8 +188,8 @@ struct Vec8<float> {
 // A warp takes (token, part): part `p` of `parts` of the token's heads.  A row's D/16 lanes (padded
 // to `lanes`, a power of two) hold two 8-element vectors each: lane l < rot/16 the vectors l and
 // l + rot/16 of the rotated elements, the others two of the rest.
-template <typename T, bool kInterleaved, int kUnroll>
-__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeCall c, int lanes_log2,
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __grid_constant__ RopeCall c, int lanes_log2,
                                                            int parts) {
   __shared__ __align__(16) float2 cs_sh[kWarpsPerBlock][kRopeMaxD / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -180,25 +206,92 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant
   griddep_wait();
   griddep_release();
 
-  // weights of the normalised tensors (at most the first two) at this lane's elements
-  float2 ga[2][4], gb[2][4];
+  // weights of the normalised tensors (at most the first two)
+  __shared__ __align__(16) float gamma_sh[2][kRopeMaxD];
+  __shared__ double freq_sh[4 * kRopeMaxD / 2];
+  for (int e = threadIdx.x; e < c.n_axes * half; e += kThreads) freq_sh[e] = c.freq[e];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const bool have = t < c.n_tensors && c.t[t].gamma != nullptr && live;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ga[t][i] = have ? *reinterpret_cast<const float2*>(c.t[t].gamma + va + 2 * i) : make_float2(0.f, 0.f);
-      gb[t][i] = have ? *reinterpret_cast<const float2*>(c.t[t].gamma + vb + 2 * i) : make_float2(0.f, 0.f);
-    }
-  }
+  for (int t = 0; t < 2; ++t)
+    if (t < c.n_tensors && c.t[t].gamma != nullptr && int(threadIdx.x) < D) gamma_sh[t][threadIdx.x] = c.t[t].gamma[threadIdx.x];
+  __syncthreads();
 
-  const long long n_items = (long long)c.tokens * parts;
-  const long long n_warps = (long long)gridDim.x * kWarpsPerBlock;
-  for (long long item = (long long)blockIdx.x * kWarpsPerBlock + warp; item < n_items; item += n_warps) {
-    const int token = int(item / parts), part = int(item - (long long)token * parts);
-    const int pr = token % c.pos_rows;
+  const int n_items = c.tokens * parts;  // the launcher keeps it below 2^31 less the grid's warps
+  const int n_warps = int(gridDim.x) * kWarpsPerBlock;
+  const int first = int(blockIdx.x) * kWarpsPerBlock + warp;
+
+  // Loads run kStages - 1 steps (of one warp-load of rows) ahead, over tensors and tokens alike;
+  // a lane reads back only what it copied itself, so a stage needs no barrier.
+  extern __shared__ __align__(16) uint8_t ring[];
+  using V = Vec8<T>;
+  constexpr int kStageBytes = 2 * V::kSlots * 512, kStages = V::kStages;
+  constexpr int kRingBytes = kStages * kStageBytes;
+  uint8_t* slots = ring + warp * kRingBytes + lane * 16;
+  const uint32_t slots_u32 = smem_u32(slots);
+  int f_item = first, f_tensor = 0;  // the next step to fetch: item, tensor, first head
+  int f_part = first % parts, f_head = 0, f_end = 0;
+  const T* f_src = nullptr;
+  auto heads_of = [&](int ti, int part, int& h_begin, int& h_end) {
+    const unsigned heads = unsigned(c.t[ti].heads);
+    h_begin = parts == 1 ? 0 : int(heads * unsigned(part) / unsigned(parts));
+    h_end = parts == 1 ? int(heads) : int(heads * unsigned(part + 1) / unsigned(parts));
+  };
+  auto open = [&]() {  // f_item's token and tensor
+    heads_of(f_tensor, f_part, f_head, f_end);
+    const int token = parts == 1 ? f_item : f_item / parts;
+    f_src = static_cast<const T*>(c.t[f_tensor].src) + (long long)token * c.t[f_tensor].src_stride;
+  };
+  auto settle = [&]() {  // on to the next tensor or item that has a head left
+    while (f_head >= f_end) {
+      if (++f_tensor >= c.n_tensors) {
+        f_tensor = 0;
+        f_item += n_warps;
+        if (f_item >= n_items) return;
+        f_part = parts == 1 ? 0 : f_item % parts;
+      }
+      open();
+    }
+  };
+  auto fetch = [&](int stage) {
+    if (f_item < n_items) {
+      const int h = f_head + sub;
+      if (live && h < f_end) {
+        V::fetch(slots_u32 + stage * kStageBytes, f_src + h * D + va);
+        V::fetch(slots_u32 + stage * kStageBytes + kStageBytes / 2, f_src + h * D + vb);
+      }
+      f_head += rows_per_warp;
+      settle();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (f_item < n_items) {
+    open();
+    settle();
+  }
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  // lane a holds axis a's position of the next item, loaded one item ahead
+  auto position = [&](int item) {
+    const int row = (parts == 1 ? item : item / parts) % c.pos_rows;
+    return lane < c.n_axes ? c.pos[(long long)row * c.n_axes + lane] : 0;
+  };
+  int next_pos = first < n_items ? position(first) : 0;
+  int stage = 0;
+  for (int item = first; item < n_items; item += n_warps) {
+    const int token = parts == 1 ? item : item / parts;
+    const int part = item - token * parts;
+    const int pos = next_pos;
+    if (item + n_warps < n_items) next_pos = position(item + n_warps);
     __syncwarp();  // the previous token's angles are read no more
-    for (int p = lane; p < half; p += 32) cs[p] = pair_angle(c, pr, p);
+    for (int p0 = 0; p0 < half; p0 += 32) {
+      const int p = p0 + lane;
+      double angle = 0.0;
+      for (int a = 0; a < c.n_axes; ++a) {
+        const int at = __shfl_sync(0xffffffffu, pos, a);
+        if (p < half) angle = fma(double(at), freq_sh[a * half + p], angle);
+      }
+      if (p < half) cs[p] = turn_by(angle, c.factor);
+    }
     __syncwarp();
     // cos and sin of this lane's pairs: 8 l + i (halves), or 4 (va / 8) + i and 4 (vb / 8) + i
     float2 w[8];
@@ -207,83 +300,81 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant
       for (int i = 0; i < 8; ++i)
         w[i] = cs[kInterleaved ? (i < 4 ? va / 2 + i : vb / 2 + i - 4) : va + i];
     }
-#pragma unroll
-    for (int ti = 0; ti < 3; ++ti) {
-      if (ti >= c.n_tensors) break;
+    for (int ti = 0; ti < c.n_tensors; ++ti) {
       const RopeTensor& t = c.t[ti];
-      const T* src = static_cast<const T*>(t.src) + (long long)token * t.src_stride;
       T* dst = static_cast<T*>(t.dst) + (long long)token * t.dst_stride;
-      const int h_begin = int((long long)t.heads * part / parts), h_end = int((long long)t.heads * (part + 1) / parts);
-      for (int h0 = h_begin; h0 < h_end; h0 += rows_per_warp * kUnroll) {
-        Vec8<T> xa[kUnroll], xb[kUnroll];
+      const bool norm = t.gamma != nullptr, rotate = t.rotate;
+      int h0, h_end;
+      heads_of(ti, part, h0, h_end);
+      for (; h0 < h_end; h0 += rows_per_warp) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        V xa, xb;
+        xa.load(slots + stage * kStageBytes);
+        xb.load(slots + stage * kStageBytes + kStageBytes / 2);
+        fetch(stage == 0 ? kStages - 1 : stage - 1);  // the stage read in the step before
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        const int h = h0 + sub;
+        const bool on = live && h < h_end;
+        if (norm || rotate) {  // otherwise the rows only move, bit for bit
+          float2 a[4], b[4];
+          xa.get(a);
+          xb.get(b);
+          if (norm) {
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int h = h0 + u * rows_per_warp + sub;
-          if (live && h < h_end) {
-            xa[u].load(src + (long long)h * D + va);
-            xb[u].load(src + (long long)h * D + vb);
+            for (int i = 0; i < 4; ++i) s2 = ffma2(b[i], b[i], ffma2(a[i], a[i], s2));
+            float ss = on ? s2.x + s2.y : 0.f;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+              if (o < (1 << lanes_log2)) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float mean = ss * inv_d + c.eps;
+            const float r = mean > 0.f ? rsqrt_refined(mean) : 0.f;  // a zero row with eps = 0 stays 0
+            const float2 r2 = make_float2(r, r), os = make_float2(c.out_scale, c.out_scale);
+            const float4* ga = reinterpret_cast<const float4*>(&gamma_sh[ti & 1][live ? va : 0]);
+            const float4* gb = reinterpret_cast<const float4*>(&gamma_sh[ti & 1][live ? vb : 0]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 p = ga[i], q = gb[i];
+              a[2 * i] = fmul2(fmul2(fmul2(a[2 * i], r2), make_float2(p.x, p.y)), os);
+              a[2 * i + 1] = fmul2(fmul2(fmul2(a[2 * i + 1], r2), make_float2(p.z, p.w)), os);
+              b[2 * i] = fmul2(fmul2(fmul2(b[2 * i], r2), make_float2(q.x, q.y)), os);
+              b[2 * i + 1] = fmul2(fmul2(fmul2(b[2 * i + 1], r2), make_float2(q.z, q.w)), os);
+            }
           }
+          if (turns && rotate) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kInterleaved) {  // (x0 c - x1 s, x1 c + x0 s)
+                const float2 x = a[i], y = b[i], wa = w[i], wb = w[4 + i];
+                a[i] = ffma2(x, make_float2(wa.x, wa.x), fmul2(make_float2(x.y, x.x), make_float2(-wa.y, wa.y)));
+                b[i] = ffma2(y, make_float2(wb.x, wb.x), fmul2(make_float2(y.y, y.x), make_float2(-wb.y, wb.y)));
+              } else {  // pairs 2i and 2i + 1: a cos - b sin, b cos + a sin
+                const float2 x = a[i], y = b[i];
+                const float2 co = make_float2(w[2 * i].x, w[2 * i + 1].x);
+                const float2 si = make_float2(w[2 * i].y, w[2 * i + 1].y);
+                a[i] = ffma2(x, co, fmul2(y, make_float2(-si.x, -si.y)));
+                b[i] = ffma2(y, co, fmul2(x, si));
+              }
+            }
+          }
+          xa.set(a);
+          xb.set(b);
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          if (h0 + u * rows_per_warp >= h_end) break;  // the whole warp
-          const int h = h0 + u * rows_per_warp + sub;
-          const bool on = live && h < h_end;
-          if (ti < 2 && (t.gamma != nullptr || t.rotate)) {  // the third tensor only moves
-            float2 a[4], b[4];
-            xa[u].get(a);
-            xb[u].get(b);
-            if (t.gamma != nullptr) {
-              float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s2 = ffma2(b[i], b[i], ffma2(a[i], a[i], s2));
-              float ss = on ? s2.x + s2.y : 0.f;
-#pragma unroll
-              for (int o = 1; o < 16; o <<= 1)
-                if (o < (1 << lanes_log2)) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              const float mean = ss * inv_d + c.eps;
-              const float r = mean > 0.f ? rsqrt_refined(mean) : 0.f;  // a zero row with eps = 0 stays 0
-              const float2 r2 = make_float2(r, r), os = make_float2(c.out_scale, c.out_scale);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = fmul2(fmul2(fmul2(a[i], r2), ga[ti & 1][i]), os);
-                b[i] = fmul2(fmul2(fmul2(b[i], r2), gb[ti & 1][i]), os);
-              }
-            }
-            if (turns && t.rotate) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (kInterleaved) {  // (x0 c - x1 s, x1 c + x0 s)
-                  const float2 x = a[i], y = b[i], wa = w[i], wb = w[4 + i];
-                  a[i] = ffma2(x, make_float2(wa.x, wa.x), fmul2(make_float2(x.y, x.x), make_float2(-wa.y, wa.y)));
-                  b[i] = ffma2(y, make_float2(wb.x, wb.x), fmul2(make_float2(y.y, y.x), make_float2(-wb.y, wb.y)));
-                } else {  // pairs 2i and 2i + 1: a cos - b sin, b cos + a sin
-                  const float2 x = a[i], y = b[i];
-                  const float2 co = make_float2(w[2 * i].x, w[2 * i + 1].x);
-                  const float2 si = make_float2(w[2 * i].y, w[2 * i + 1].y);
-                  a[i] = ffma2(x, co, fmul2(y, make_float2(-si.x, -si.y)));
-                  b[i] = ffma2(y, co, fmul2(x, si));
-                }
-              }
-            }
-            xa[u].set(a);
-            xb[u].set(b);
-          }
-          if (on) {
-            const int g = t.group_magic == 0 ? h : int(__umulhi(unsigned(h), t.group_magic));  // h / group
-            T* d = dst + g * t.group_stride + (long long)(h - g * t.group) * D;
-            xa[u].store(d + va);
-            xb[u].store(d + vb);
-          }
+        if (on) {
+          const int g = t.group_magic == 0 ? h : int(__umulhi(unsigned(h), t.group_magic));  // h / group
+          T* d = dst + g * t.group_stride + (long long)(h - g * t.group) * D;
+          xa.store(d + va);
+          xb.store(d + vb);
         }
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T>
 cudaError_t launch_vector(const RopeCall& c, int max_heads, cudaStream_t stream) {
-  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+  auto kernel = c.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>;
   int lanes_log2 = 0;
   while ((1 << lanes_log2) < c.D / 16) ++lanes_log2;
   const int rows_per_warp = 32 >> lanes_log2;
@@ -293,18 +384,21 @@ cudaError_t launch_vector(const RopeCall& c, int max_heads, cudaStream_t stream)
   int parts = 1;
   while (c.tokens * parts < want && parts * rows_per_warp < max_heads) parts *= 2;
   const long long blocks = ((long long)c.tokens * parts + kWarpsPerBlock - 1) / kWarpsPerBlock;
-  const long long cap = (long long)sm_count() * 2;
+  const long long cap = (long long)sm_count() * kBlocksPerSm;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(blocks < cap ? blocks : cap));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWarpsPerBlock * Vec8<T>::kStages * 2 * Vec8<T>::kSlots * 512;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, c.interleaved ? rope_kernel<T, true, kUnroll> : rope_kernel<T, false, kUnroll>, c,
-                            lanes_log2, parts);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(cfg.dynamicSmemBytes));
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, kernel, c, lanes_log2, parts);
 }
 
 // Can the vector form take this call?  Whole vectors, every row on 16 bytes.
