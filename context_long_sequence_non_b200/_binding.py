@@ -432,48 +432,57 @@ def head2seq(src, P, out=None, stream=None):
 # ------------------------------------------------------------------ windowed attention
 
 
-def _call(device, stream, what, fn, *args):
-    """Run a library call with ``device`` current (the library launches on the current device)
-    on ``stream``, or on that device's current stream."""
+# The current stream and device, without the wrapper objects (these calls are a few microseconds
+# of host time in all, and the wrappers were four of them).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(index, stream, what, fn, *args):
+    """Run a library call with CUDA device ``index`` current (the library launches on the current
+    device) on ``stream``, or on that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+        raw = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+        raw = stream.cuda_stream
+    if _current_device() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
     if st != OK:
         raise CpattnError(st, what)
 
 
 def _same_device(first, *ts):
+    """The CUDA device index that every tensor is on."""
     if not first.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
+    index = first.get_device()
     for t in ts:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must live on one CUDA device")
+    return index
 
 
-def _token_stride(t, name, dims=4):
+def _token_stride(t, name):
     """Elements between consecutive tokens of a [..., tokens, heads, D] tensor whose heads are
     packed and whose tokens are evenly spaced through every leading axis."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != dims and dims:
-        raise ValueError(f"{name} must have {dims} axes")
+    shape = t.shape
     D, H = shape[-1], shape[-2]
-    if t.numel() == 0:
+    if t.is_contiguous():
         return H * D
+    stride = t.stride()
     if (D > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    step, count = None, 1  # `count` tokens below this axis, `step` apart once one axis shows it
+    step, count = None, 1  # tokens are `step` apart; `count` of them below the axis at hand
     for n, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n > 1:
             if step is None:
-                if st % count:
-                    raise ValueError(f"{name}: tokens must be evenly spaced")
-                step = st // count
+                step = st
             elif st != step * count:
                 raise ValueError(f"{name}: tokens must be evenly spaced")
         count *= n
@@ -485,8 +494,11 @@ def _token_stride(t, name, dims=4):
 
 
 def _packed(t, shape, name, dtype):
-    _need_shape(t, shape, name, dtype)
-    if t is not None and not t.is_contiguous():
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -506,7 +518,7 @@ def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
         raise ValueError("k and v must be [B][Skv][Hkv][D] matching q")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype")
-    strides = tuple(_token_stride(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    strides = (_token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
     if kv_len is not None:
         _packed(kv_len, (B,), "kv_len", torch.int32)
     if out is None:
@@ -517,11 +529,10 @@ def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
         _packed(lse, (B, H, Sq), "lse", torch.float32)
     elif want_lse:
         lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
-    _same_device(q, k, v, kv_len, out, lse)
+    index = _same_device(q, k, v, kv_len, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr())
-    return ptrs, (B, H, Hkv, Sq, Skv, D), strides, float(scale), out, lse
+    return index, (B, H, Hkv, Sq, Skv, D) + strides, float(scale), out, lse
 
 
 def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=None, out=None,
@@ -536,11 +547,10 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
     (out, lse).  Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
     if accumulate and (out is None or lse is None):
         raise ValueError("accumulate needs the running out and lse")
-    ptrs, dims, strides, scale, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype,
-                                                        want_lse)
-    _call(q.device, stream, "cpattn_window_fwd", lib().cpattn_window_fwd, *ptrs, out.data_ptr(),
-          None if lse is None else lse.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
-          *dims, *strides, scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
+    index, dims, scale, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
+    _call(index, stream, "cpattn_window_fwd", lib().cpattn_window_fwd, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+          None if kv_len is None else kv_len.data_ptr(), *dims, scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
           _extent(left, "left"), _extent(right, "right"), _extent(sinks, "sinks"),
           _dtype_code(q.dtype), _dtype_code(out.dtype), 1 if accumulate else 0)
     return out, lse
@@ -551,11 +561,11 @@ def window_decode(q, k_cache, v_cache, kv_len=None, left=-1, sinks=0, out=None, 
     """The last Sq tokens of each sequence against its cache (causal, window and sinks as
     window_fwd): q [B][Sq][H][D], caches [B][S_max][Hkv][D], ``kv_len`` int32 [B] the tokens each
     sequence holds, the newest included (None: S_max).  See cpattn_window_decode."""
-    ptrs, dims, strides, scale, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale,
-                                                        out_dtype, want_lse)
-    _call(q.device, stream, "cpattn_window_decode", lib().cpattn_window_decode, *ptrs,
-          None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), *dims, *strides, scale, _extent(left, "left"),
+    index, dims, scale, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale, out_dtype,
+                                                want_lse)
+    _call(index, stream, "cpattn_window_decode", lib().cpattn_window_decode, q.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
+          out.data_ptr(), None if lse is None else lse.data_ptr(), *dims, scale, _extent(left, "left"),
           _extent(sinks, "sinks"), _dtype_code(q.dtype), _dtype_code(out.dtype))
     return out, lse
 
@@ -620,10 +630,10 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _need_shape(out, x.shape, "out", x.dtype)
-    _same_device(x, pos, freq, out)
-    _call(x.device, stream, "cpattn_rope", lib().cpattn_rope, x.data_ptr(), out.data_ptr(),
+    index = _same_device(x, pos, freq, out)
+    _call(index, stream, "cpattn_rope", lib().cpattn_rope, x.data_ptr(), out.data_ptr(),
           pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes, 1 if interleaved else 0,
-          float(factor), _token_stride(x, "x", 0), _token_stride(out, "out", 0), _dtype_code(x.dtype))
+          float(factor), _token_stride(x, "x"), _token_stride(out, "out"), _dtype_code(x.dtype))
     return out
 
 
@@ -645,13 +655,13 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.
     qo, ko = out
     _need_shape(qo, q.shape, "out[0]", q.dtype)
     _need_shape(ko, k.shape, "out[1]", k.dtype)
-    _same_device(q, k, gamma_q, gamma_k, pos, freq, qo, ko)
-    _call(q.device, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope, q.data_ptr(),
+    index = _same_device(q, k, gamma_q, gamma_k, pos, freq, qo, ko)
+    _call(index, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope, q.data_ptr(),
           k.data_ptr(), qo.data_ptr(), ko.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(),
           pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2], k.shape[-2], D, rot, axes,
           1 if interleaved else 0, float(eps), float(out_scale), float(factor),
-          _token_stride(q, "q", 0), _token_stride(k, "k", 0), _token_stride(qo, "out[0]", 0),
-          _token_stride(ko, "out[1]", 0), _dtype_code(q.dtype))
+          _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(qo, "out[0]"),
+          _token_stride(ko, "out[1]"), _dtype_code(q.dtype))
     return qo, ko
 
 
@@ -680,8 +690,8 @@ def seq2head_qkv_norm_rope(q, k, v, P, gamma_q, gamma_k, pos, freq, interleaved=
     for t in (q, k, v):
         if not t.is_contiguous():
             raise ValueError("q, k, v must be contiguous")
-    _same_device(q, k, v, gamma_q, gamma_k, pos, freq, *out)
-    _call(q.device, stream, "cpattn_seq2head_qkv_norm_rope", lib().cpattn_seq2head_qkv_norm_rope,
+    index = _same_device(q, k, v, gamma_q, gamma_k, pos, freq, *out)
+    _call(index, stream, "cpattn_seq2head_qkv_norm_rope", lib().cpattn_seq2head_qkv_norm_rope,
           q.data_ptr(), k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out),
           None if gamma_q is None else gamma_q.data_ptr(),
           None if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H,

@@ -24,6 +24,7 @@
 
 #include <cstdint>
 
+#include "api_common.h"
 #include "kernels.h"
 #include "norm_math.cuh"
 #include "rope.h"
@@ -395,8 +396,8 @@ cudaError_t launch_vector(const RopeCall& c, int max_heads, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(cfg.dynamicSmemBytes));
+  static SmemOptIn opt_in[2];
+  const cudaError_t e = opt_in[c.interleaved](reinterpret_cast<const void*>(kernel), int(cfg.dynamicSmemBytes));
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kernel, c, lanes_log2, parts);
 }

@@ -47,8 +47,8 @@ __device__ __forceinline__ int sequence_length(const WindowCall& c, int b) {
   return n < 0 ? 0 : (n > c.Skv ? c.Skv : n);
 }
 
-// One warp per query row on the CUDA cores: any D <= 256, bf16 or fp32 inputs.
-cudaError_t launch_window_rows(const WindowCall& c, cudaStream_t stream);
+// fp32 inputs, D <= 256, both forms (no accumulate).
+cudaError_t launch_window_f32(const WindowCall& c, cudaStream_t stream);
 
 // Tensor-core kernel: bf16 inputs, D 64 or 128, Skv >= 1.
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream);

@@ -99,7 +99,7 @@ int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, fl
                     (c.left >= 0 && c.sinks == 0 && c.off - c.left >= Skv);
   if (c.accumulate && none) return CPATTN_OK;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (c.in_f32) return cuda_status(cpattn::launch_window_rows(c, cs));
+  if (c.in_f32) return cuda_status(cpattn::launch_window_f32(c, cs));
   if (Skv == 0)
     return cuda_status(cpattn::launch_fill_empty(out, size_t(B) * Sq * H * D * elem_size(out_dtype), lse,
                                                  size_t(B) * H * Sq, cs));
@@ -119,7 +119,7 @@ int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache
   if (S_max < 1) return CPATTN_ERR_SHAPE;
   if (sinks > S_max) c.sinks = S_max;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(c.in_f32 ? cpattn::launch_window_rows(c, cs) : cpattn::launch_window_decode(c, cs));
+  return cuda_status(c.in_f32 ? cpattn::launch_window_f32(c, cs) : cpattn::launch_window_decode(c, cs));
 }
 
 }  // extern "C"

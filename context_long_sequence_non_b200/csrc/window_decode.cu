@@ -26,6 +26,7 @@
 
 #include <cstdint>
 
+#include "api_common.h"
 #include "kernels.h"
 #include "sm100_ptx.cuh"
 #include "window.h"
@@ -355,7 +356,8 @@ int decode_cluster(long long groups, long long most_keys, int keys_per_chunk) {
 template <int D, bool kOutF32>
 cudaError_t launch(const WindowCall& c, cudaStream_t stream) {
   auto kernel = window_decode_kernel<D, kOutF32>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Decode<D>::kSmem);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Decode<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int row_tiles = (c.H / c.Hkv * c.Sq + kRows - 1) / kRows;
   const long long groups = (long long)c.B * c.Hkv * row_tiles;

@@ -535,7 +535,8 @@ template <int D, bool kOutF32, bool kAcc>
 cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    int* err, cudaStream_t stream) {
   auto kernel = window_sm100_kernel<D, kOutF32, kAcc>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geometry<D>::kSmem);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int n_tiles = (c.Sq + kBlockM - 1) / kBlockM;
   cudaLaunchConfig_t cfg = {};

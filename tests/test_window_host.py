@@ -232,7 +232,7 @@ def test_window_binding_checks():
 
 
 def test_token_strides():
-    ts = lambda x, dims=0: B._token_stride(x, "x", dims)
+    ts = lambda x: B._token_stride(x, "x")
     assert ts(t(2, 5, 4, 64)) == 256
     assert ts(t(2, 5, 12, 64)[:, :, 4:8]) == 768
     assert ts(t(7, 12, 64)[:, :1]) == 768
