@@ -15,9 +15,9 @@
 // shared memory -- one launch, no workspace, a fixed order of sums.  The cluster is as large as
 // needed to occupy the GPU (decode_cluster below).
 //
-// Loads.  Each warp keeps kStages chunks in flight with 16-byte cp.async (16 keys of D = 128 or
-// 32 of D = 64: 8 KB of K and V), 192 KB per SM at two CTAs, rows swizzled so that ldmatrix
-// reads without bank conflicts.  Early (sink) keys and window keys form one list, so no chunk is
+// Loads.  Each warp keeps kStages chunks of 16 keys in flight with 16-byte cp.async, 192 KB per SM
+// (two CTAs of D = 128, four of D = 64), rows swizzled so that ldmatrix reads without bank
+// conflicts.  Early (sink) keys and window keys form one list, so no chunk is
 // spent on a boundary; rows that no query sees are never read, and the list's end is filled
 // with zeros.
 #include <cooperative_groups.h>
@@ -37,7 +37,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;  // (token, head) rows of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -72,7 +72,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 template <int D>
 struct Decode {
-  static constexpr int kKeys = D == 128 ? 16 : 32;  // keys of a chunk
+  static constexpr int kKeys = 16;  // keys of a chunk
+  static constexpr int kStages = 3, kCtas = D == 128 ? 2 : 4;  // chunks in flight, CTAs per SM
   static constexpr int kRowBytes = D * 2;
   static constexpr int kVecs = D / 8;  // 16-byte vectors of a row
   static constexpr int kTile = kKeys * kRowBytes;
@@ -91,9 +92,10 @@ __device__ __forceinline__ uint32_t swz(int r, int v) {
 }
 
 template <int D, bool kOutF32>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
     window_decode_kernel(const __grid_constant__ WindowCall c, int row_tiles, float scale_log2) {
   using T = Decode<D>;
+  constexpr int kStages = T::kStages;
   constexpr int kN = T::kKeys / 8;  // 8-key column tiles of S
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
@@ -317,17 +319,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // ---- fold the cluster: each block finishes every n_ranks-th group of four columns
   for (int e = int(threadIdx.x) * n_ranks + rank; e < n_rows * (D / 4); e += kWarps * 32 * n_ranks) {
     const int r = e / (D / 4), d = 4 * (e % (D / 4));
-    float top = -INFINITY;
-    for (int k = 0; k < n_ranks; ++k) top = fmaxf(top, *cluster.map_shared_rank(&cta_m[r], k));
-    float sum = 0.f;
+    float mk[kMaxCluster], lk[kMaxCluster];
+    float4 xk[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {  // every remote read in flight at once
+      mk[k] = -INFINITY;
+      lk[k] = 0.f;
+      xk[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n_ranks) {
+        mk[k] = *cluster.map_shared_rank(&cta_m[r], k);
+        lk[k] = *cluster.map_shared_rank(&cta_l[r], k);
+        xk[k] = *cluster.map_shared_rank(reinterpret_cast<float4*>(co + r * T::kOStride + d), k);
+      }
+    }
+    float top = mk[0], sum = 0.f;
+#pragma unroll
+    for (int k = 1; k < kMaxCluster; ++k) top = fmaxf(top, mk[k]);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n_ranks; ++k) {
-      const float mk = *cluster.map_shared_rank(&cta_m[r], k);
-      if (mk == -INFINITY) continue;  // saw no key
-      const float w = ex2(mk - top);
-      sum = fmaf(w, *cluster.map_shared_rank(&cta_l[r], k), sum);
-      const float4 x = *cluster.map_shared_rank(reinterpret_cast<float4*>(co + r * T::kOStride + d), k);
-      a.x = fmaf(w, x.x, a.x), a.y = fmaf(w, x.y, a.y), a.z = fmaf(w, x.z, a.z), a.w = fmaf(w, x.w, a.w);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      const float w = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - top);  // 0: that block saw no key
+      sum = fmaf(w, lk[k], sum);
+      a.x = fmaf(w, xk[k].x, a.x), a.y = fmaf(w, xk[k].y, a.y), a.z = fmaf(w, xk[k].z, a.z), a.w = fmaf(w, xk[k].w, a.w);
     }
     const float inv = top == -INFINITY ? 0.f : 1.0f / sum;  // no visible key: O = 0, LSE = -inf
     const int row = row0 + r, i = row / G, h = kvh * G + (row - i * G);
@@ -344,13 +357,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (n_ranks > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
 
-// CTAs that share a (sequence, key head, row tile).  Enough for kCtasPerSm CTAs on every SM, as
-// long as each keeps at least two chunks per warp of the most keys the window can hold.
-int decode_cluster(long long groups, long long most_keys, int keys_per_chunk) {
-  const long long want = 4LL * sm_count();
-  int n = 1;
-  while (n < 8 && groups * n < want && most_keys >= 2LL * n * kWarps * keys_per_chunk) n *= 2;
-  return n;
+// CTAs that share a (sequence, key head, row tile): the count that minimises the modelled time.
+// A CTA takes a fixed f (start, first loads, fold; more with a cluster to meet) and t for each
+// chunk of its warps, t the chunk's latency or the share of an SM's bandwidth that its CTAs
+// leave; when there is more than one wave of CTAs, half a CTA's time is lost at the end.
+// Calibrated on a B200 (f = 3 or 4 us, t >= 0.6 us, 44 bytes per ns and SM): it picks the
+// fastest of 1, 2, 4 and 8 on eight shapes from 8 to 1024 groups, where the wrong count costs
+// from 10% to 9 times (1024 groups of 200 keys: 15 us with one CTA each, 67 us with eight).
+template <int D>
+int decode_cluster(long long groups, long long most_keys) {
+  using T = Decode<D>;
+  const double sms = sm_count();
+  int best = 1;
+  double best_t = 0;
+  for (int n = 1; n <= kMaxCluster; n *= 2) {
+    const double ctas = double(groups) * n;
+    const double per_sm = ctas / sms < 1 ? 1 : (ctas / sms > T::kCtas ? T::kCtas : ctas / sms);
+    const double share = per_sm * kWarps * T::kStage / 44e3;  // us per chunk at full bandwidth
+    const long long chunks = (most_keys + T::kKeys - 1) / T::kKeys;
+    const double own = double((chunks + kWarps * n - 1) / (kWarps * n));
+    const double cta = (n > 1 ? 4.0 : 3.0) + own * (share > 0.6 ? share : 0.6);
+    const double waves = ctas / (sms * T::kCtas);
+    const double t = (waves <= 1 ? 1.0 : waves + 0.5) * cta;
+    if (n == 1 || t < best_t) best = n, best_t = t;
+  }
+  return best;
 }
 
 template <int D, bool kOutF32>
@@ -363,7 +394,7 @@ cudaError_t launch(const WindowCall& c, cudaStream_t stream) {
   const long long groups = (long long)c.B * c.Hkv * row_tiles;
   long long most = c.Skv;
   if (c.left >= 0 && (long long)c.sinks + c.left + c.Sq < most) most = (long long)c.sinks + c.left + c.Sq;
-  const int n = decode_cluster(groups, most, Decode<D>::kKeys);
+  const int n = decode_cluster<D>(groups, most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(groups * n));
   cfg.blockDim = dim3(kWarps * 32);
