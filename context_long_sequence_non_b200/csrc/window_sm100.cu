@@ -12,12 +12,25 @@
 // be a large share of its life if nothing ran beside them; with two independent CTAs one's
 // softmax, start and end overlap the other's matrix products, and a tile visits its own key
 // blocks and no neighbour's.  The price, K and V not shared between two query tiles, is L2
-// traffic of 64 KB per 128 x 128 block, under half of what L2 delivers.
+// traffic of 64 KB per 128 x 128 block, under half of what L2 delivers.  Blocks start at the
+// first key that the tile sees, not at a multiple of 128: a window of 4096 costs 33 blocks.
 //   warps 0-3  softmax, one thread per query row = TMEM lane
-//   warp  4    TMA producer: Q, then per block K (one ring) and V in two 64-key halves (another)
+//   warp  4    TMA producer: Q, then per block K (one ring) and V in two 64-key halves (another);
+//              the first loads leave before the CTA's warps have met
 //   warp  5    TMEM allocator; clears V rows that no row of the tile sees (below); one of its
 //              threads issues every tcgen05.mma
 // TMEM (256 columns): S (128 fp32; P written back over it as bf16 pairs) | O (D fp32).
+// The bf16 epilogue leaves through shared memory and one TMA store a tile.
+//
+// What bounds it.  A block costs a CTA about 3300 cycles with its neighbour running: softmax 1900
+// (exponentials on the special-function unit and the packed FMAs around them), P V and the next
+// Q K^T 700 to 1000, wake-ups 500; the tensor pipe is busy 61% of them.  At the large sizes the
+// card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x 16 heads, causal
+// window 4096 with 64 sinks, 1.52 ms = 945 TFLOP/s of visible products; 4608 x 24, 512 to either
+// side with 512 sinks, 104 us = 760 TFLOP/s.  Tried and not kept, same cases: two 128-row tiles
+// in one CTA with shared K and V, one CTA per item (1.55 ms, 109 us; 40% slower at 333 rows) and
+// persistent over items (1.80 ms); D = 64 with P in TMEM of its own, so that S runs ahead (no
+// change); 1, 3 or 4 of every 8 exponential pairs on the FMA pipe (-1 to 0, +2, +4% time).
 //
 // Hidden keys.  A block is masked per element only where some row of the warp does not see all
 // of it.  A hidden key's weight is exactly 0 or, on the polynomial's clamp, at most 2^-125 of a
@@ -58,7 +71,7 @@ struct Geometry {
   static constexpr int kVBytes = kBoxes * kVBoxBytes;
   // K blocks and V halves in flight: what two CTAs per SM leave room for
   static constexpr int kK = D == 128 ? 1 : 2;
-  static constexpr int kV = D == 128 ? 3 : 4;
+  static constexpr int kV = D == 128 ? 2 : 4;
   static constexpr int kOffK = kTileBytes;
   static constexpr int kOffV = kOffK + kK * kTileBytes;
   static constexpr int kOffBars = kOffV + kV * kVBytes;
@@ -123,6 +136,18 @@ __device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, 
   return t;
 }
 
+// 4-D tiled tensor store shared -> global, and the wait until the shared memory has been read.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // the low n bits, n clamped to 0..32
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
@@ -132,60 +157,67 @@ template <int D, bool kOutF32, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 2)
     window_sm100_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowCall c,
-                        int n_tiles, float scale_log2, float rescale_log2, int* err,
-                        long long wait_limit) {
+                        const __grid_constant__ CUtensorMap tm_o, float scale_log2, float rescale_log2,
+                        int* err, long long wait_limit) {
   using G = Geometry<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Barriers& bars = *reinterpret_cast<Barriers*>(smem + G::kOffBars);
   const uint32_t smem_base = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // CTAs run in index order, so the tiles with the most keys (the last ones, when the window
-  // grows with the position) come first within each head and the grid ends on short ones
-  const int tile = n_tiles - 1 - int(blockIdx.x % unsigned(n_tiles));
-  const int bh = int(blockIdx.x / unsigned(n_tiles));
-  const int b = bh / c.H, h = bh - b * c.H;
-  const int kvh = h / (c.H / c.Hkv);
+  // CTAs run in index order, x fastest, so the tiles with the most keys (the last ones, when the
+  // window grows with the position) come first within each head and the grid ends on short ones
+  const int tile = int(gridDim.x) - 1 - int(blockIdx.x);
+  const int h = blockIdx.y, b = blockIdx.z;
   const int q_first = tile * kBlockM;
   volatile int* abort_flag = &bars.abort;
 
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars.q_full), 1);
-    mbar_init(smem_u32(&bars.s_full), 1);
-    mbar_init(smem_u32(&bars.o_full), 1);
-    mbar_init(smem_u32(&bars.drain), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.p_part[i]), 4);  // one arrive per softmax warp
-      mbar_init(smem_u32(&bars.k_full[i]), 1);
-      mbar_init(smem_u32(&bars.k_empty[i]), 1);
+  if (warp == kWarpProducer) {
+    if (lane == 0) {
+      mbar_init(smem_u32(&bars.q_full), 1);
+      mbar_init(smem_u32(&bars.s_full), 1);
+      mbar_init(smem_u32(&bars.o_full), 1);
+      mbar_init(smem_u32(&bars.drain), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&bars.p_part[i]), 4);  // one arrive per softmax warp
+        mbar_init(smem_u32(&bars.k_full[i]), 1);
+        mbar_init(smem_u32(&bars.k_empty[i]), 1);
+      }
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(smem_u32(&bars.v_full[i]), 1);
+        mbar_init(smem_u32(&bars.v_empty[i]), 1);
+      }
+      bars.abort = 0;
+      fence_mbar_init();
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&bars.v_full[i]), 1);
-      mbar_init(smem_u32(&bars.v_empty[i]), 1);
-    }
-    bars.abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == kWarpProducer && lane == 0) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
-  if (warp == kWarpMma) {
+    __syncwarp();
+  } else if (warp == kWarpMma) {
     tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
     tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_release();
+  const int len = sequence_length(c, b);
+  const int off = c.off;
+  const int last_row = min(q_first + kBlockM, c.Sq) - 1;
+  const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len);
+  // The first loads go out before the block meets: nothing waits on their barriers earlier, and
+  // their latency covers the rest of the set-up.
+  const int kvh = c.Hkv == c.H ? h : h / (c.H / c.Hkv);
+  if (warp == kWarpProducer && blk.n > 0 && lane == 0) {
+    const uint32_t bar_q = smem_u32(&bars.q_full), bar_k = smem_u32(&bars.k_full[0]);
+    mbar_arrive_expect_tx(bar_k, G::kTileBytes);
+    mbar_arrive_expect_tx(bar_q, G::kTileBytes);
+#pragma unroll
+    for (int bx = 0; bx < G::kBoxes; ++bx) {
+      tma_load_4d(smem_base + bx * G::kBoxBytes, &tm_q, bar_q, bx * 64, h, q_first, b);
+      tma_load_4d(smem_base + G::kOffK + bx * G::kBoxBytes, &tm_k, bar_k, bx * 64, kvh, blk.base(0), b);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  griddep_wait();
-  griddep_release();
-
-  const int len = sequence_length(c, b);
-  const int off = c.from_end ? len - c.Sq : c.off;
-  const int last_row = min(q_first + kBlockM, c.Sq) - 1;
-  const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len);
 
   if (warp < 4) {
     // ------------------------------------------------------------------ softmax warps
@@ -214,15 +246,31 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < kBlockN; ++e) x[e] = __uint_as_float(t[e]);
       }
       const int kb = blk.base(j);
-      const bool sees_all = (kb >= r.lo && kb + kBlockN <= r.hi) || kb + kBlockN <= r.early;
+      const bool sees_all = ((kb >= r.lo || r.early >= r.lo) && kb + kBlockN <= r.hi) || kb + kBlockN <= r.early;
       if (!__all_sync(0xffffffffu, sees_all)) {
+        const int early = r.early - kb, lo = r.lo - kb, hi = r.hi - kb;  // in columns of the block
+        if (__any_sync(0xffffffffu, early > 0 && early < lo)) {
+          // early keys, a gap, and maybe window keys: a bit per column
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int k0 = kb + 32 * w;
-          const uint32_t see = (low_bits(r.hi - k0) & ~low_bits(r.lo - k0)) | low_bits(r.early - k0);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t see = (low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w)) | low_bits(early - 32 * w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(see & (1u << e))) x[32 * w + e] = -INFINITY;
+            for (int e = 0; e < 32; ++e)
+              if (!(see & (1u << e))) x[32 * w + e] = -INFINITY;
+          }
+        } else {
+          // the window's ends (early keys, if any, run into it): usually one of them per block
+          const int from = early >= lo ? 0 : lo;
+          if (__any_sync(0xffffffffu, from > 0)) {
+#pragma unroll
+            for (int e = 0; e < kBlockN; ++e)
+              if (e < from) x[e] = -INFINITY;
+          }
+          if (__any_sync(0xffffffffu, hi < kBlockN)) {
+#pragma unroll
+            for (int e = 0; e < kBlockN; ++e)
+              if (e >= hi) x[e] = -INFINITY;
+          }
         }
       }
       float mx;
@@ -334,6 +382,33 @@ __global__ void __launch_bounds__(kThreads, 2)
           lse_out = (mx + log2f(tot)) * kLn2;
         }
       }
+      if constexpr (!kOutF32 && !kAcc) {
+        // bf16 rows go to global memory as one tile: each thread writes its row into Q's shared
+        // memory (read for the last time before O was complete) in the 128-byte swizzle, and a TMA
+        // store takes it from there, leaving out rows past Sq.  Row-by-row stores, 32 rows of
+        // 16 bytes an instruction, kept the warps 2700 cycles and more.
+        const uint32_t row_addr = smem_base + uint32_t(row) * 128u;
+#pragma unroll 1
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t t[32];
+          if (blk.n > 0) tmem_ld32(t_o + oc * 32, t);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = empty ? 0u : pack_bf16x2(__uint_as_float(t[8 * e + 2 * i]) * fc,
+                                              __uint_as_float(t[8 * e + 2 * i + 1]) * fc);
+            const uint32_t v = uint32_t((oc & 1) * 4 + e);  // 16-byte vector of the 64-column box
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             row_addr + uint32_t(oc >> 1) * G::kBoxBytes + ((v ^ (uint32_t(row) & 7u)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
+        }
+        if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
+        fence_proxy_async_smem();
+      } else {
 #pragma unroll 1
       for (int oc = 0; oc < D / 32; ++oc) {
         uint32_t t[32];
@@ -384,31 +459,39 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
+        if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
+      }
+    }
+    if constexpr (!kOutF32 && !kAcc) {
+      // every softmax warp comes here, also one whose wait ran out
+      if (bar_and(1, 128, ok) && threadIdx.x == 0) {
+#pragma unroll
+        for (int bx = 0; bx < G::kBoxes; ++bx)
+          tma_store_4d(&tm_o, smem_base + bx * G::kBoxBytes, bx * 64, h, q_first, b);
+        tma_store_wait();
+      }
     }
   } else if (warp == kWarpProducer) {
     // ------------------------------------------------------------------ TMA producer
-    if (blk.n > 0 && elect_one()) {
+    if (blk.n > 0 && lane == 0) {
       const uint32_t bar_q = smem_u32(&bars.q_full);
-      mbar_arrive_expect_tx(bar_q, G::kTileBytes);
-#pragma unroll
-      for (int bx = 0; bx < G::kBoxes; ++bx)
-        tma_load_4d(smem_base + bx * G::kBoxBytes, &tm_q, bar_q, bx * 64, h, q_first, b);
-      int k_issued = 0, v_issued = 0;
+      int k_issued = 1, v_issued = 0;  // K of block 0 and Q are on their way
       bool go = true;
       for (int j = 0; go && j < blk.n; ++j) {
         const int kb = blk.base(j);
         const int ks = j % G::kK;
-        if (!mbar_wait(smem_u32(&bars.k_empty[ks]), (uint32_t(j / G::kK) & 1u) ^ 1u, abort_flag, err,
-                       wait_limit))
-          break;
-        const uint32_t bar_k = smem_u32(&bars.k_full[ks]);
-        mbar_arrive_expect_tx(bar_k, G::kTileBytes);
+        if (j > 0) {
+          if (!mbar_wait(smem_u32(&bars.k_empty[ks]), (uint32_t(j / G::kK) & 1u) ^ 1u, abort_flag, err,
+                         wait_limit))
+            break;
+          const uint32_t bar_k = smem_u32(&bars.k_full[ks]);
+          mbar_arrive_expect_tx(bar_k, G::kTileBytes);
 #pragma unroll
-        for (int bx = 0; bx < G::kBoxes; ++bx)
-          tma_load_4d(smem_base + G::kOffK + ks * G::kTileBytes + bx * G::kBoxBytes, &tm_k, bar_k, bx * 64,
-                      kvh, kb, b);
-        k_issued = j + 1;
+          for (int bx = 0; bx < G::kBoxes; ++bx)
+            tma_load_4d(smem_base + G::kOffK + ks * G::kTileBytes + bx * G::kBoxBytes, &tm_k, bar_k, bx * 64,
+                        kvh, kb, b);
+          k_issued = j + 1;
+        }
         for (int half = 0; half < 2; ++half) {
           const int use = 2 * j + half, vs = use % G::kV;
           if (!mbar_wait(smem_u32(&bars.v_empty[vs]), (uint32_t(use / G::kV) & 1u) ^ 1u, abort_flag, err,
@@ -435,71 +518,90 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------------ MMA issuer
-    // the whole warp walks the loop (it clears hidden V rows together); `leader` issues
+    // one thread issues; the whole warp only meets to clear hidden V rows
     if (blk.n > 0) {
       const bool leader = elect_one();
       constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, true);
+      const uint64_t q_desc = sdesc_sw128(smem_base, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_base + G::kOffK, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_base + G::kOffV, G::kVBoxBytes, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return bool(__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, err, wait_limit)));
+        return mbar_wait(smem_u32(bar), parity & 1u, abort_flag, err, wait_limit);
       };
       // S = Q K^T over D in K = 16 steps: 32 bytes per step inside a 128-byte swizzled row, the
       // next 64 columns in the next box
       auto issue_qk = [&](int ks) {
-        if (!leader) return;
-        const uint32_t k_addr = smem_base + G::kOffK + ks * G::kTileBytes;
-        tc_fence_after();
+        const uint64_t kd = k_desc + uint32_t(ks * (G::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * G::kBoxBytes + (kk & 3) * 32;
-          mma_ss(tmem, sdesc_sw128(smem_base + o, 16, 1024), sdesc_sw128(k_addr + o, 16, 1024), idesc_qk,
-                 kk > 0 ? 1u : 0u);
+          const uint32_t o = ((kk >> 2) * G::kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss(tmem, q_desc + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
         }
         tc_commit(smem_u32(&bars.s_full));
         tc_commit(smem_u32(&bars.k_empty[ks]));
       };
-      bool ok = wait(&bars.q_full, 0) && wait(&bars.k_full[0], 0);
-      if (ok) issue_qk(0);
-      for (int j = 0; ok && j < blk.n; ++j) {
+      bool ok = true;
+      if (leader) {
+        ok = wait(&bars.q_full, 0) && wait(&bars.k_full[0], 0);
+        if (ok) {
+          tc_fence_after();
+          issue_qk(0);
+        }
+      }
+      for (int j = 0; j < blk.n; ++j) {
         const int kb = blk.base(j);
+        const int v0 = (2 * j) % G::kV;  // slots v0 and v0 + 1 (kV is even)
+        const uint32_t v_ph = uint32_t(2 * j / G::kV);
+        const int k1 = min(kb + kBlockN, c.Skv);  // rows past Skv arrive as 0
+        if (!blk.all_seen(kb, k1)) {
+          bool landed = wait(&bars.v_full[v0], v_ph) && wait(&bars.v_full[v0 + 1], v_ph);
+          landed = __all_sync(0xffffffffu, landed);
+          // the hidden rows are [early, lo) and [hi, ..) of the block: whole 128-byte rows of each
+          // box, whatever the swizzle, so runs of 16-byte stores
+          auto clear = [&](int r0, int r1) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int use = 2 * j + half, vs = use % G::kV;
-          const uint32_t v_off = G::kOffV + vs * G::kVBytes;
-          ok = ok && wait(&bars.v_full[vs], uint32_t(use / G::kV) & 1u);
-          const int k0 = kb + half * kHalf, k1 = min(k0 + kHalf, c.Skv);  // rows past Skv arrive as 0
-          if (ok && k0 < k1 && !blk.all_seen(k0, k1)) {
-            for (int rr = lane >> 3; rr < k1 - k0; rr += 4) {
-              const int key = k0 + rr;
-              if (key < blk.early || (key >= blk.lo && key < blk.hi)) continue;
+            for (int half = 0; half < 2; ++half) {
+              const int a = max(r0 - half * kHalf, 0) * 128, z = min(r1 - half * kHalf, kHalf) * 128;
+              uint8_t* v = smem + G::kOffV + (v0 + half) * G::kVBytes;
+              for (int o = a + lane * 16; o < z; o += 512)
 #pragma unroll
-              for (int bx = 0; bx < G::kBoxes; ++bx)  // a whole 128-byte row: any swizzle
-                *reinterpret_cast<uint4*>(smem + v_off + bx * G::kVBoxBytes + rr * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+                for (int bx = 0; bx < G::kBoxes; ++bx)
+                  *reinterpret_cast<uint4*>(v + bx * G::kVBoxBytes + o) = make_uint4(0u, 0u, 0u, 0u);
             }
-            fence_proxy_async_smem();  // the tensor core reads the zeros
-            __syncwarp();
+          };
+          if (landed) {
+            clear(max(blk.early - kb, 0), min(blk.lo, k1) - kb);
+            clear(max(blk.hi - kb, 0), k1 - kb);
           }
-          ok = ok && wait(&bars.p_part[half], uint32_t(j) & 1u);
-          if (!ok) break;
-          // O += P V over 64 keys in K = 16 steps: P from TMEM (8 columns per step), V MN-major
-          // (16 key rows = 2 KB per step, the next 64 columns of D in the next box)
-          if (leader) {
+          fence_proxy_async_smem();  // the tensor core reads the zeros
+          __syncwarp();
+        }
+        if (leader && ok) {
+          // everything but P is waited for first: between P's arrival and the products there is
+          // nothing but their issue
+          const bool more = j + 1 < blk.n;
+          const int ks = (j + 1) % G::kK;
+          ok = wait(&bars.v_full[v0], v_ph) && wait(&bars.v_full[v0 + 1], v_ph);
+          const uint64_t vd = v_desc + uint32_t(v0 * (G::kVBytes >> 4));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1 && more) ok = ok && wait(&bars.k_full[ks], uint32_t((j + 1) / G::kK));
+            ok = ok && wait(&bars.p_part[half], uint32_t(j));
+            if (!ok) break;
             tc_fence_after();
+            // O += P V over 64 keys in K = 16 steps: P from TMEM (8 columns per step), V MN-major
+            // (16 key rows = 2 KB per step, the next 64 columns of D in the next box)
 #pragma unroll
             for (int kk = 0; kk < kHalf / 16; ++kk)
               mma_ts(tmem + kBlockN, tmem + half * kHalfPairs + kk * 8,
-                     sdesc_sw128(smem_base + v_off + kk * 16 * 128, G::kVBoxBytes, 1024), idesc_pv,
+                     vd + uint32_t((half * G::kVBytes + kk * 16 * 128) >> 4), idesc_pv,
                      (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(smem_u32(&bars.v_empty[vs]));
+            tc_commit(smem_u32(&bars.v_empty[v0 + half]));
           }
+          if (ok && more) issue_qk(ks);
         }
-        if (!ok) break;
-        if (j + 1 < blk.n) {
-          const int ks = (j + 1) % G::kK;
-          ok = wait(&bars.k_full[ks], uint32_t((j + 1) / G::kK) & 1u);
-          if (ok) issue_qk(ks);
-        }
+        __syncwarp();
       }
       if (leader) {
         if (ok) tc_commit(smem_u32(&bars.o_full));
@@ -533,14 +635,13 @@ bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long 
 
 template <int D, bool kOutF32, bool kAcc>
 cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   int* err, cudaStream_t stream) {
+                   const CUtensorMap& to, int* err, cudaStream_t stream) {
   auto kernel = window_sm100_kernel<D, kOutF32, kAcc>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
-  const int n_tiles = (c.Sq + kBlockM - 1) / kBlockM;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(n_tiles) * c.H * c.B);
+  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM), unsigned(c.H), unsigned(c.B));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Geometry<D>::kSmem;
   cfg.stream = stream;
@@ -549,29 +650,33 @@ cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, n_tiles, float(double(c.scale) * 1.4426950408889634074),
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, to,
+                            float(double(c.scale) * 1.4426950408889634074),
                             kRescaleLog2, err, kDefaultWaitLimit);
 }
 
 template <int D>
 cudaError_t launch_d(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                     int* err, cudaStream_t stream) {
+                     const CUtensorMap& to, int* err, cudaStream_t stream) {
   if (c.out_f32)
-    return c.accumulate ? launch<D, true, true>(c, tq, tk, tv, err, stream)
-                        : launch<D, true, false>(c, tq, tk, tv, err, stream);
-  return c.accumulate ? launch<D, false, true>(c, tq, tk, tv, err, stream)
-                      : launch<D, false, false>(c, tq, tk, tv, err, stream);
+    return c.accumulate ? launch<D, true, true>(c, tq, tk, tv, to, err, stream)
+                        : launch<D, true, false>(c, tq, tk, tv, to, err, stream);
+  return c.accumulate ? launch<D, false, true>(c, tq, tk, tv, to, err, stream)
+                      : launch<D, false, false>(c, tq, tk, tv, to, err, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream) {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM) ||
       !encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
       !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kHalf))
     return cudaErrorInvalidValue;
-  return c.D == 128 ? launch_d<128>(c, tq, tk, tv, err, stream) : launch_d<64>(c, tq, tk, tv, err, stream);
+  // bf16 results leave by TMA; the other forms do not use the map
+  if (c.out_f32 || c.accumulate) to = tq;
+  else if (!encode(&to, c.out, c.B, c.Sq, c.H, c.D, (long long)c.H * c.D, kBlockM)) return cudaErrorInvalidValue;
+  return c.D == 128 ? launch_d<128>(c, tq, tk, tv, to, err, stream) : launch_d<64>(c, tq, tk, tv, to, err, stream);
 }
 
 }  // namespace cpattn
