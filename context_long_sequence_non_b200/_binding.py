@@ -470,12 +470,11 @@ def _same_device(first, *ts):
 
 def _token_stride(t, name):
     """Elements between consecutive tokens of a [..., tokens, heads, D] tensor whose heads are
-    packed and whose tokens are evenly spaced through every leading axis."""
-    shape = t.shape
-    D, H = shape[-1], shape[-2]
+    packed and whose tokens are evenly spaced through every leading axis (0: packed tokens)."""
     if t.is_contiguous():
-        return H * D
-    stride = t.stride()
+        return 0
+    shape, stride = t.shape, t.stride()
+    D, H = shape[-1], shape[-2]
     if (D > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     step, count = None, 1  # tokens are `step` apart; `count` of them below the axis at hand
@@ -487,19 +486,20 @@ def _token_stride(t, name):
                 raise ValueError(f"{name}: tokens must be evenly spaced")
         count *= n
     if step is None:
-        return H * D
+        return 0
     if step < H * D:
         raise ValueError(f"{name}: tokens must not overlap")
     return step
 
 
 def _packed(t, shape, name, dtype):
+    if t.shape == shape and (dtype is None or t.dtype == dtype) and t.is_contiguous():
+        return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _extent(n, name, least=-(1 << 31)):
@@ -510,19 +510,20 @@ def _extent(n, name, least=-(1 << 31)):
 
 
 def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
-    if q.dim() != 4 or k.dim() != 4:
+    kv_shape, dtype = k.shape, q.dtype
+    if q.dim() != 4 or len(kv_shape) != 4:
         raise ValueError("q, k and v must be [B][S][H][D]")
     B, Sq, H, D = q.shape
-    Skv, Hkv = k.shape[1], k.shape[2]
-    if k.shape != (B, Skv, Hkv, D) or v.shape != k.shape:
+    Bk, Skv, Hkv, Dk = kv_shape
+    if Bk != B or Dk != D or v.shape != kv_shape:
         raise ValueError("k and v must be [B][Skv][Hkv][D] matching q")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("q, k and v must have one dtype")
     strides = (_token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
     if kv_len is not None:
         _packed(kv_len, (B,), "kv_len", torch.int32)
     if out is None:
-        out = torch.empty((B, Sq, H, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = torch.empty((B, Sq, H, D), dtype=out_dtype or dtype, device=q.device)
     else:
         _packed(out, (B, Sq, H, D), "out", out_dtype)
     if lse is not None:
@@ -604,36 +605,38 @@ def rope_axes(freqs):
 
 
 def _rope_args(tokens, pos, freq):
-    if freq.dtype != torch.float64 or freq.dim() not in (1, 2) or not freq.is_contiguous():
+    f, p = freq.shape, pos.shape
+    if freq.dtype != torch.float64 or not 1 <= len(f) <= 2 or not freq.is_contiguous():
         raise ValueError("freq must be a contiguous float64 [rot/2] or [axes][rot/2]")
-    axes = 1 if freq.dim() == 1 else freq.shape[0]
+    axes = 1 if len(f) == 1 else f[0]
     if pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ValueError("pos must be contiguous int32")
-    if axes == 0 or pos.numel() % axes or (pos.dim() > 1 and pos.shape[-1] != axes) or (
-            pos.dim() < 2 and axes > 1):
+    if axes == 0 or (len(p) > 1 and p[-1] != axes) or (len(p) < 2 and axes > 1):
         raise ValueError("pos must be [rows] or [..., rows, axes] matching freq")
     rows = pos.numel() // axes
     if tokens and (rows < 1 or tokens % rows):
         raise ValueError("the tokens must be a multiple of pos's rows")
-    return rows, axes, 2 * freq.shape[-1]
+    return rows, axes, 2 * f[-1]
 
 
 def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
     """Rotary positions of x [..., tokens, H, D] (bf16 or fp32): the first rot elements of every
     head turn by ``pos @ freq`` (pos int32 [rows] or [rows][axes], freq float64 [rot/2] or
     [axes][rot/2]); ``out=x`` rotates in place.  See cpattn_rope."""
-    if x.dim() < 3:
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 3:
         raise ValueError("x must be [..., tokens, H, D]")
-    H, D = x.shape[-2:]
-    tokens = x.shape[:-2].numel()
+    H, D = shape[-2], shape[-1]
+    tokens = shape[0] if len(shape) == 3 else shape[:-2].numel()
     rows, axes, rot = _rope_args(tokens, pos, freq)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need_shape(out, x.shape, "out", x.dtype)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    elif out.shape != shape or out.dtype != dtype:
+        _need_shape(out, shape, "out", dtype)
     index = _same_device(x, pos, freq, out)
     _call(index, stream, "cpattn_rope", lib().cpattn_rope, x.data_ptr(), out.data_ptr(),
           pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes, 1 if interleaved else 0,
-          float(factor), _token_stride(x, "x"), _token_stride(out, "out"), _dtype_code(x.dtype))
+          float(factor), _token_stride(x, "x"), _token_stride(out, "out"), _dtype_code(dtype))
     return out
 
 

@@ -170,6 +170,35 @@ def test_seq2head_norm_rope(P, S_l, H, D, rot, norm):
     assert torch.equal(qh, q3) and torch.equal(kh, k3)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_tokens_and_repeated_positions(interleaved):
+    # more tokens than warps on the GPU, three sequences at the same positions
+    x = randn(31, 3, 2500, 3, 64)
+    pos = torch.randint(0, 1 << 20, (2500, 2), generator=torch.Generator().manual_seed(1)).int()
+    freq = cp.rope_axes([cp.rope_frequencies(32)[0], cp.rope_frequencies(16)[0]])
+    want = ow.rotate(x, pos.numpy(), freq, interleaved)
+    got = cp.rope(x.to(DEV), pos.to(DEV), freq.to(DEV), interleaved=interleaved)
+    torch.cuda.synchronize()
+    check(got, want, _f64(x), 48, interleaved, 1.0)
+
+
+def test_many_head_groups():
+    P, S_l, H, D = 7, 3, 70, 32
+    q, k, v = (randn(P + i, P, S_l, H, D) for i in range(3))
+    g = torch.ones(D)
+    T = P * S_l
+    pos = torch.arange(T, dtype=torch.int32) * 11
+    freq, _ = cp.rope_frequencies(D)
+    qh, kh, vh = cp.seq2head_qkv_norm_rope(*(t.to(DEV) for t in (q, k, v)), P, g.to(DEV), g.to(DEV), pos.to(DEV),
+                                           freq.to(DEV))
+    torch.cuda.synchronize()
+    n = ow.rms_norm(q, g)
+    check(qh, oref.seq2head(ow.rotate(n, pos.numpy(), freq), P), oref.seq2head(n, P), D, False, 1.0)
+    n = ow.rms_norm(k, g)
+    check(kh, oref.seq2head(ow.rotate(n, pos.numpy(), freq), P), oref.seq2head(n, P), D, False, 1.0)
+    assert torch.equal(vh.cpu().view(torch.int16), torch.from_numpy(oref.seq2head(v.view(torch.int16).numpy(), P)))
+
+
 def test_margins_of_a_strided_output_are_left_alone():
     x = randn(3, 50, 2, 64)
     freq = cp.rope_frequencies(64, device=DEV)[0]

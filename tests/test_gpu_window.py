@@ -177,6 +177,41 @@ def test_f32(D, sizes, w):
     run_window(q, k, v, kv_len=[sizes[1] // 2, 0], q_pos=20, k_pos=10, out_dtype=torch.bfloat16, **w)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_f32_many_rows(D):
+    # enough 64-row blocks for two per SM: the wide form of the fp32 kernel
+    q, k, v = make(21, 2, 8, 2, 1300, 1300, D, dtype=torch.float32)
+    run_window(q, k, v, left=40, right=9, sinks=3)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    r = np.random.default_rng(1000 + seed)
+    pick = lambda *a: a[int(r.integers(len(a)))]
+    D, Hkv = pick(64, 128), pick(1, 2, 3)
+    Sq, Skv = int(r.integers(1, 600)), int(r.integers(1, 900))
+    q, k, v = make(seed, pick(1, 2), Hkv * pick(1, 2, 5), Hkv, Sq, Skv, D, sigma=pick(1.0, 1.0, 3.0))
+    B = q.shape[0]
+    w = dict(left=pick(-1, int(r.integers(0, 700))), right=pick(-1, 0, int(r.integers(0, 300))),
+             sinks=pick(0, 4, int(r.integers(0, 500))), q_pos=int(r.integers(0, 900)), k_pos=int(r.integers(0, 300)))
+    kv_len = [int(x) for x in r.integers(0, Skv + 1, B)] if pick(True, False) else None
+    run_window(q, k, v, kv_len=kv_len, out_dtype=pick(torch.bfloat16, torch.float32), **w)
+    q1 = q[:, :min(Sq, pick(1, 1, 2, 7))].contiguous()
+    run_decode(q1, k, v, [int(x) for x in r.integers(0, Skv + 1, B)], left=w["left"], sinks=w["sinks"])
+
+
+def test_without_lse():
+    q, k, v = (x.to(DEV) for x in make(22, 1, 4, 2, 200, 200, 64))
+    o, l = cp.window_fwd(q, k, v, left=30, right=0, want_lse=False)
+    o2, _ = cp.window_fwd(q, k, v, left=30, right=0)
+    d, l3 = cp.window_decode(q[:, -1:].contiguous(), k, v, left=30, want_lse=False)
+    d2, _ = cp.window_decode(q[:, -1:].contiguous(), k, v, left=30)
+    f, l4 = cp.window_fwd(q.float(), k.float(), v.float(), left=30, right=0, want_lse=False)
+    torch.cuda.synchronize()
+    assert l is None and l3 is None and l4 is None
+    assert torch.equal(o, o2) and torch.equal(d, d2) and torch.isfinite(f).all()
+
+
 @pytest.mark.parametrize("acc_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("w", [dict(left=150, right=100, sinks=6), dict(left=-1, right=0), dict(left=70, right=0)])
 def test_ring_step(acc_dtype, w):

@@ -233,12 +233,13 @@ def test_window_binding_checks():
 
 def test_token_strides():
     ts = lambda x: B._token_stride(x, "x")
-    assert ts(t(2, 5, 4, 64)) == 256
+    assert ts(t(2, 5, 4, 64)) == 0  # packed
     assert ts(t(2, 5, 12, 64)[:, :, 4:8]) == 768
     assert ts(t(7, 12, 64)[:, :1]) == 768
-    assert ts(t(1, 1, 12, 64)[:, :, :4]) == 256  # one token: any spacing will do
-    assert ts(t(4, 9, 2, 64)[1:2, 3:]) == 128
-    assert ts(t(0, 2, 64)) == 128
+    assert ts(t(1, 1, 12, 64)[:, :, :4]) == 0  # one token: any spacing will do
+    assert ts(t(4, 9, 2, 64)[1:2, 3:]) == 0
+    assert ts(t(0, 2, 64)) == 0
+    assert ts(t(0, 12, 64)[:, :4]) == 0
     for bad in (t(2, 5, 64, 4).transpose(2, 3), t(1, 2, 64).expand(3, 2, 64), t(5, 2, 4, 64).transpose(0, 1),
                 t(3, 6, 2, 64)[:, ::2].flip(0)[:, :2]):
         with pytest.raises(ValueError):
