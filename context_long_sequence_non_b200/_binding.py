@@ -70,7 +70,7 @@ def lib() -> ctypes.CDLL:
             L.cpattn_seq2head_qkv_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f,
                                                    f, vp]
             d = ctypes.c_double
-            L.cpattn_window_fwd.argtypes = [vp] * 6 + [i] * 6 + [ll] * 3 + [f] + [i] * 8 + [vp]
+            L.cpattn_window_fwd.argtypes = [vp] * 7 + [i] * 6 + [ll] * 3 + [f] + [i] * 8 + [vp]
             L.cpattn_window_decode.argtypes = [vp] * 6 + [i] * 6 + [ll] * 3 + [f] + [i] * 4 + [vp]
             L.cpattn_rope_frequencies.argtypes = [vp, vp, i, d, i, d, d, d, d]
             L.cpattn_rope.argtypes = [vp] * 4 + [i] * 7 + [f, ll, ll, i, vp]
@@ -537,7 +537,7 @@ def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
 
 
 def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=None, out=None,
-               lse=None, scale=None, out_dtype=None, want_lse=True, accumulate=False, stream=None):
+               lse=None, scale=None, out_dtype=None, want_lse=True, accumulate=False, run=None, stream=None):
     """Attention limited to a window: the query at position p = q_pos + i sees the keys at
     positions p - left .. p + right (-1: no bound on that side) and, up to p + right, those below
     ``sinks``; see cpattn_window_fwd.
@@ -545,13 +545,20 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
     q: [B][Sq][H][D], k/v: [B][Skv][Hkv][D] with H a multiple of Hkv (bf16 -> tensor-core kernel,
     D 64 or 128; fp32 -> CUDA-core kernel, D <= 256); their heads may be slices of a wider row.
     ``kv_len``: int32 [B], keys of each sequence.  ``accumulate`` merges into the running
-    (out, lse).  Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
-    if accumulate and (out is None or lse is None):
+    (out, lse), or merges the running (``run`` float32, lse) into a bf16 ``out``.  Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
+    if accumulate and (lse is None or (out is None and run is None)):
         raise ValueError("accumulate needs the running out and lse")
+    if run is not None:
+        if not accumulate:
+            raise ValueError("run is the running result of an accumulating call")
+        _packed(run, q.shape, "run", torch.float32)
     index, dims, scale, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
+    if run is not None:
+        _same_device(q, run)
     _call(index, stream, "cpattn_window_fwd", lib().cpattn_window_fwd, q.data_ptr(), k.data_ptr(),
           v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-          None if kv_len is None else kv_len.data_ptr(), *dims, scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
+          None if kv_len is None else kv_len.data_ptr(), None if run is None else run.data_ptr(), *dims,
+          scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
           _extent(left, "left"), _extent(right, "right"), _extent(sinks, "sinks"),
           _dtype_code(q.dtype), _dtype_code(out.dtype), 1 if accumulate else 0)
     return out, lse

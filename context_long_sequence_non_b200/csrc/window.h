@@ -18,6 +18,7 @@ struct WindowCall {
   void* out;
   float* lse;
   const int* kv_len;
+  const float* o_run;  // accumulate: the running O, when it is not `out` itself
   int B, H, Hkv, Sq, Skv, D;
   long long q_stride, k_stride, v_stride;  // elements between tokens; a batch is S tokens
   float scale;
@@ -50,7 +51,7 @@ __device__ __forceinline__ int sequence_length(const WindowCall& c, int b) {
 // fp32 inputs, D <= 256, both forms (no accumulate).
 cudaError_t launch_window_f32(const WindowCall& c, cudaStream_t stream);
 
-// Tensor-core kernel: bf16 inputs, D 64 or 128, Skv >= 1.
+// Tensor-core kernel: bf16 inputs, D 64 or 128.
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream);
 
 // Single-token form (from_end, right = 0): bf16 inputs, D 64 or 128.

@@ -82,14 +82,20 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
 extern "C" {
 
 int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
-                      const int* kv_len, int B, int H, int Hkv, int Sq, int Skv, int D,
+                      const int* kv_len, const float* o_run, int B, int H, int Hkv, int Sq, int Skv, int D,
                       long long q_stride, long long k_stride, long long v_stride, float scale,
                       int q_pos, int k_pos, int left, int right, int sinks, int in_dtype,
                       int out_dtype, int accumulate, cpattn_stream_t stream) {
-  WindowCall c{q, k, v, out, lse, kv_len, B, H, Hkv, Sq, Skv, D, q_stride, k_stride, v_stride, scale,
+  WindowCall c{q, k, v, out, lse, kv_len, o_run, B, H, Hkv, Sq, Skv, D, q_stride, k_stride, v_stride, scale,
                0, clamp_extent(left), clamp_extent(right), sinks, false, false, false, accumulate != 0};
   const int st = check(&c, in_dtype, out_dtype);
   if (st != CPATTN_OK) return st;
+  if (o_run != nullptr) {
+    if (accumulate == 0 || out_dtype != CPATTN_BF16) return CPATTN_ERR_UNSUPPORTED;
+    if (!aligned(o_run, 16)) return CPATTN_ERR_ALIGN;
+    const size_t n = size_t(B) * Sq * H * D, lb = size_t(B) * H * Sq * 4;
+    if (overlap(o_run, n * 4, out, n * 2) || overlap(o_run, n * 4, lse, lb)) return CPATTN_ERR_SHAPE;
+  }
   if (q_pos < 0 || k_pos < 0 || q_pos >= kMaxPos - Sq || k_pos >= kMaxPos - Skv) return CPATTN_ERR_SHAPE;
   c.off = q_pos - k_pos;
   c.sinks = sinks <= k_pos ? 0 : (sinks - k_pos < Skv ? sinks - k_pos : Skv);
@@ -97,10 +103,10 @@ int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   const int last = c.off + Sq - 1;
   const bool none = Skv == 0 || (c.right >= 0 && last + c.right < 0) ||
                     (c.left >= 0 && c.sinks == 0 && c.off - c.left >= Skv);
-  if (c.accumulate && none) return CPATTN_OK;
+  if (c.accumulate && none && o_run == nullptr) return CPATTN_OK;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (c.in_f32) return cuda_status(cpattn::launch_window_f32(c, cs));
-  if (Skv == 0)
+  if (Skv == 0 && !c.accumulate)
     return cuda_status(cpattn::launch_fill_empty(out, size_t(B) * Sq * H * D * elem_size(out_dtype), lse,
                                                  size_t(B) * H * Sq, cs));
   int* err = cpattn::device_error_word();
@@ -112,7 +118,7 @@ int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache
                          void* out, float* lse, int B, int H, int Hkv, int Sq, int S_max, int D,
                          long long q_stride, long long k_stride, long long v_stride, float scale,
                          int left, int sinks, int in_dtype, int out_dtype, cpattn_stream_t stream) {
-  WindowCall c{q, k_cache, v_cache, out, lse, kv_len, B, H, Hkv, Sq, S_max, D, q_stride, k_stride,
+  WindowCall c{q, k_cache, v_cache, out, lse, kv_len, nullptr, B, H, Hkv, Sq, S_max, D, q_stride, k_stride,
                v_stride, scale, 0, clamp_extent(left), 0, sinks, true, false, false, false};
   const int st = check(&c, in_dtype, out_dtype);
   if (st != CPATTN_OK) return st;

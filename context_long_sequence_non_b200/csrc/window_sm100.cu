@@ -153,13 +153,21 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-template <int D, bool kOutF32, bool kAcc>
+// What becomes of a tile's result.
+enum Result : int {
+  kWrite = 0,       // written
+  kMerge = 1,       // merged into the running (out, lse) in place
+  kMergeFrom32 = 2  // merged with the running (o_run fp32, lse) into bf16 out
+};
+
+template <int D, bool kOutF32, int kResult>
 __global__ void __launch_bounds__(kThreads, 2)
     window_sm100_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowCall c,
                         const __grid_constant__ CUtensorMap tm_o, float scale_log2, float rescale_log2,
                         int* err, long long wait_limit) {
   using G = Geometry<D>;
+  constexpr bool kAcc = kResult != kWrite;
   extern __shared__ __align__(1024) uint8_t smem[];
   Barriers& bars = *reinterpret_cast<Barriers*>(smem + G::kOffBars);
   const uint32_t smem_base = smem_u32(smem);
@@ -371,15 +379,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       float lse_out = empty ? -INFINITY : lc2 * kLn2;
       bool write = in_range;
       if constexpr (kAcc) {
-        if (empty) write = false;  // nothing to add: the running row stays as it is
+        if (kResult == kMerge && empty) write = false;  // nothing to add: the running row stays as it is
         if (write) {
-          const float la2 = c.lse[lse_idx] * kLog2e;
-          const float mx = fmaxf(la2, lc2);
-          const float wa = exp2f(la2 - mx), wc = exp2f(lc2 - mx);
-          const float tot = wa + wc;
-          fa = wa / tot;
-          fc = wc / (tot * l);
-          lse_out = (mx + log2f(tot)) * kLn2;
+          const float la = c.lse[lse_idx];
+          if (empty) {  // the running row alone, rounded (0 when it is empty too)
+            fa = la == -INFINITY ? 0.f : 1.f;
+            lse_out = la;
+          } else {
+            const float la2 = la * kLog2e;
+            const float mx = fmaxf(la2, lc2);
+            const float wa = exp2f(la2 - mx), wc = exp2f(lc2 - mx);
+            const float tot = wa + wc;
+            fa = wa / tot;
+            fc = wc / (tot * l);
+            lse_out = (mx + log2f(tot)) * kLn2;
+          }
         }
       }
       if constexpr (!kOutF32 && !kAcc) {
@@ -441,7 +455,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(t[8 * e + i]) * fc;
-            if (kAcc && fa != 0.f) {
+            if (kResult == kMergeFrom32 && fa != 0.f) {
+              const float4* run = reinterpret_cast<const float4*>(c.o_run + row_off + oc * 32 + e * 8);
+              const float4 a = run[0], z = run[1];
+              o[0] = fmaf(fa, a.x, o[0]), o[1] = fmaf(fa, a.y, o[1]), o[2] = fmaf(fa, a.z, o[2]), o[3] = fmaf(fa, a.w, o[3]);
+              o[4] = fmaf(fa, z.x, o[4]), o[5] = fmaf(fa, z.y, o[5]), o[6] = fmaf(fa, z.z, o[6]), o[7] = fmaf(fa, z.w, o[7]);
+            } else if (kAcc && fa != 0.f) {
               const uint4 a = dst[e];
               const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -633,10 +652,10 @@ bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kOutF32, bool kAcc>
+template <int D, bool kOutF32, int kResult>
 cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& to, int* err, cudaStream_t stream) {
-  auto kernel = window_sm100_kernel<D, kOutF32, kAcc>;
+  auto kernel = window_sm100_kernel<D, kOutF32, kResult>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -659,19 +678,21 @@ template <int D>
 cudaError_t launch_d(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& to, int* err, cudaStream_t stream) {
   if (c.out_f32)
-    return c.accumulate ? launch<D, true, true>(c, tq, tk, tv, to, err, stream)
-                        : launch<D, true, false>(c, tq, tk, tv, to, err, stream);
-  return c.accumulate ? launch<D, false, true>(c, tq, tk, tv, to, err, stream)
-                      : launch<D, false, false>(c, tq, tk, tv, to, err, stream);
+    return c.accumulate ? launch<D, true, kMerge>(c, tq, tk, tv, to, err, stream)
+                        : launch<D, true, kWrite>(c, tq, tk, tv, to, err, stream);
+  if (!c.accumulate) return launch<D, false, kWrite>(c, tq, tk, tv, to, err, stream);
+  return c.o_run != nullptr ? launch<D, false, kMergeFrom32>(c, tq, tk, tv, to, err, stream)
+                            : launch<D, false, kMerge>(c, tq, tk, tv, to, err, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, to;
-  if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM) ||
-      !encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
-      !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kHalf))
+  if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM)) return cudaErrorInvalidValue;
+  if (c.Skv == 0) tk = tv = tq;  // no block loads through them
+  else if (!encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
+           !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kHalf))
     return cudaErrorInvalidValue;
   // bf16 results leave by TMA; the other forms do not use the map
   if (c.out_f32 || c.accumulate) to = tq;

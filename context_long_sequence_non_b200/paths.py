@@ -34,10 +34,13 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
     A window (``left`` or ``right`` not -1; see window_fwd) takes the queries at positions
     ``q_pos`` on and chunk c at ``k_pos[c]`` on (None: the chunks follow one another from 0);
     every chunk is then one cpattn_window_fwd, merged in its epilogue, and K/V may have fewer
-    heads than Q.  Returns ``(O, LSE)``.
+    heads than Q; without ``acc_dtype`` the running O is float32 and rounded to q's dtype once, by
+    the last chunk.  Returns ``(O, LSE)``.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[3])
+    # a windowed step without an acc_dtype of the caller's keeps its running O in float32
+    rounded_once = acc_dtype is None and q.dtype != torch.float32
     acc_dtype = acc_dtype or q.dtype
     Bn, Sq, H, D = q.shape
     if left >= 0 or right >= 0:
@@ -48,12 +51,16 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
             for kc in k_chunks:
                 k_pos.append(at)
                 at += kc.shape[1]
-        acc_o = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
-        acc_l = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
+        out = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
+        lse = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
+        n = len(k_chunks)
+        run = torch.empty(out.shape, dtype=torch.float32, device=q.device) if rounded_once and n > 1 else out
         for c, (kc, vc) in enumerate(zip(k_chunks, v_chunks)):
+            last = run is not out and c == n - 1
             B.window_fwd(q, kc, vc, left=left, right=right, sinks=sinks, q_pos=q_pos, k_pos=k_pos[c],
-                         out=acc_o, lse=acc_l, scale=scale, accumulate=c > 0, stream=stream)
-        return acc_o, acc_l
+                         out=out if last else run, run=run if last else None, lse=lse, scale=scale,
+                         accumulate=c > 0, stream=stream)
+        return out, lse
     acc_o = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
     acc_l = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
     if fused:

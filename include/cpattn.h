@@ -393,6 +393,10 @@ CPATTN_API int cpattn_head2seq(const void* src, void* dst, int P, int S_local, i
  * accumulate = 1 (bf16 inputs) merges the result into the running (out, lse) in place as
  *   cpattn_fwd_accumulate does; a row that sees no key keeps its running (out, lse), and a row
  *   whose running lse is -inf takes the new result without reading `out`.
+ * o_run : NULL, or (accumulate = 1, out_dtype BF16) a running O in float32, laid out as out and
+ *   not overlapping it: the result is merged with (o_run, lse) and every row of `out` is written,
+ *   rounded once (a row with running lse -inf that sees no key: 0); lse is updated in place.  It
+ *   ends a chain of chunks kept in float32.
  * 0 <= q_pos, k_pos; q_pos + Sq and k_pos + Skv below 2^30; sinks >= 0; B*Sq*H < 2^31.
  * in_dtype CPATTN_BF16: D 64 or 128; CPATTN_F32: D <= 256.  out_dtype BF16 or F32.
  * out and lse must not overlap any input.
@@ -400,7 +404,7 @@ CPATTN_API int cpattn_head2seq(const void* src, void* dst, int P, int S_local, i
  *   reported by cpattn_device_error().
  */
 CPATTN_API int cpattn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
-                                 const int* kv_len, int B, int H, int Hkv, int Sq, int Skv, int D,
+                                 const int* kv_len, const float* o_run, int B, int H, int Hkv, int Sq, int Skv, int D,
                                  long long q_stride, long long k_stride, long long v_stride,
                                  float scale, int q_pos, int k_pos, int left, int right, int sinks,
                                  int in_dtype, int out_dtype, int accumulate, cpattn_stream_t stream);

@@ -212,7 +212,7 @@ def test_without_lse():
     assert torch.equal(o, o2) and torch.equal(d, d2) and torch.isfinite(f).all()
 
 
-@pytest.mark.parametrize("acc_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("acc_dtype", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("w", [dict(left=150, right=100, sinks=6), dict(left=-1, right=0), dict(left=70, right=0)])
 def test_ring_step(acc_dtype, w):
     B, Sq, H, Hkv, D = 1, 260, 4, 2, 128
@@ -225,7 +225,35 @@ def test_ring_step(acc_dtype, w):
                                  q_pos=300, k_pos=[cuts[i] for i in order], **w)
     torch.cuda.synchronize()
     ref = ow.window_attention(q, k, v, D ** -0.5, q_pos=300, **w)
+    if acc_dtype is None:  # rounded once: the bound of a single pass, but for the merges' fp32 steps
+        o_ref, l_ref, a = ref
+        assert out.dtype == torch.bfloat16
+        S = logit_error(q, k, D ** -0.5)
+        bound = (HALF + 2e-5 + 2 * S + 4e-6) * a
+        assert (np.abs(_f64(out) - o_ref) <= bound + HALF * (np.abs(o_ref) + bound)).all()
     check(out, lse, ref, q, k, D ** -0.5, merges=4)
+
+
+def test_last_chunk_out_of_a_float32_running_result():
+    q, k, v = make(23, 1, 2, 2, 300, 100, 64)
+    run = torch.full((1, 300, 2, 64), float("nan"), device=DEV)
+    lse = torch.full((1, 2, 300), -math.inf, device=DEV)
+    run[:, 250:] = 1.001
+    lse[:, :, 250:] = 1.0
+    out = torch.full((1, 300, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    qd, kd, vd = (x.to(DEV) for x in (q, k, v))
+    cp.window_fwd(qd, kd, vd, left=20, right=0, q_pos=0, k_pos=60, out=out, lse=lse, run=run, accumulate=True)
+    torch.cuda.synchronize()
+    o, l, a = ow.window_attention(q, k, v, 0.125, 20, 0, 0, 0, 60)
+    check(out[:, 60:180], lse[:, :, 60:180], (o[:, 60:180], l[:, :, 60:180], a[:, 60:180]), q, k, 0.125)
+    assert (out[:, :60] == 0).all() and torch.isneginf(lse[:, :, :60]).all()  # empty before and after
+    assert torch.equal(out[:, 250:], run[:, 250:].bfloat16()) and (lse[:, :, 250:] == 1).all()
+    # a chunk that no row sees, and one without keys: the running result, rounded
+    for kk in (kd, kd[:, :0]):
+        out.fill_(9.0)
+        cp.window_fwd(qd, kk, kk, left=20, right=0, q_pos=1000, k_pos=0, out=out, lse=lse, run=run, accumulate=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:, 250:], run[:, 250:].bfloat16()) and (out[:, :60] == 0).all()
 
 
 def test_accumulate_keeps_rows_that_see_nothing():

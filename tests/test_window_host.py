@@ -23,10 +23,10 @@ def L():
     return B.lib()
 
 
-def window(L, q=FAKE, k=FAKE + BIG, v=FAKE + 2 * BIG, o=FAKE + 3 * BIG, lse=FAKE + 4 * BIG, kv_len=None,
+def window(L, q=FAKE, k=FAKE + BIG, v=FAKE + 2 * BIG, o=FAKE + 3 * BIG, lse=FAKE + 4 * BIG, kv_len=None, run=None,
            B_=1, H=4, Hkv=2, Sq=8, Skv=8, D=128, qs=0, ks=0, vs=0, scale=0.1, q_pos=0, k_pos=0, left=3,
            right=0, sinks=0, din=0, dout=0, acc=0):
-    return L.cpattn_window_fwd(q, k, v, o, lse, kv_len, B_, H, Hkv, Sq, Skv, D, qs, ks, vs, scale, q_pos,
+    return L.cpattn_window_fwd(q, k, v, o, lse, kv_len, run, B_, H, Hkv, Sq, Skv, D, qs, ks, vs, scale, q_pos,
                                k_pos, left, right, sinks, din, dout, acc, None)
 
 
@@ -82,6 +82,11 @@ def test_window_position_errors(L):
     assert window(L, acc=1, lse=None) == B.ERR_NULL
     assert window(L, acc=1, din=1, dout=1) == B.ERR_UNSUPPORTED
     assert decode(L, S=0) == B.ERR_SHAPE
+    assert window(L, run=FAKE + 6 * BIG) == B.ERR_UNSUPPORTED  # not an accumulating call
+    assert window(L, run=FAKE + 6 * BIG, acc=1, dout=1) == B.ERR_UNSUPPORTED
+    assert window(L, run=FAKE + 6 * BIG + 4, acc=1) == B.ERR_ALIGN
+    assert window(L, run=FAKE + 3 * BIG, acc=1) == B.ERR_SHAPE  # the running O over out
+    assert window(L, run=FAKE + 4 * BIG, acc=1) == B.ERR_SHAPE  # and over lse
     # a chunk that no row sees leaves a running result alone: nothing is launched
     assert window(L, acc=1, q_pos=100, left=3, right=0) == B.OK
     assert window(L, acc=1, k_pos=100, left=3, right=0) == B.OK
@@ -221,6 +226,10 @@ def test_window_binding_checks():
         cp.window_decode(q, k, v, kv_len=torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="running"):
         cp.window_fwd(q, k, v, accumulate=True)
+    with pytest.raises(ValueError, match="accumulating"):
+        cp.window_fwd(q, k, v, run=q.float())
+    with pytest.raises(ValueError, match="run must be"):
+        cp.window_fwd(q, k, v, run=q, accumulate=True, lse=t(2, 4, 5, dtype=torch.float32))
     with pytest.raises(ValueError, match="heads must be contiguous"):
         cp.window_fwd(t(2, 4, 5, 64).transpose(1, 2), k, v)
     with pytest.raises(ValueError, match="evenly spaced"):
