@@ -77,6 +77,22 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
   return CPATTN_OK;
 }
 
+// Which kernel serves `window_decode`: the split one, which reads a sequence's keys once for every 16
+// (token, head) rows, or, for many tokens and heads, the tensor-core one with its 128-row tiles.
+// Time per visible key: the split kernel's passes of 4 D bytes come out of L2 at 7.8 TB/s; the
+// other takes 1.65 us for each 128 keys with a tile per SM, 2.4 us with two, and so on by waves.
+// Measured with a window of 4096, split / tiles: 8 sequences x 32 heads on 8, D = 128, 64 / 82 us
+// at 16 tokens, 138 / 81 at 32; 1 x 16 heads on 16, 36 / 56 at 128 tokens; 4 x 8 heads on 1, D = 64,
+// 42 / 47 at 128.
+bool tiles_serve(const WindowCall& c) {
+  const double sms = cpattn::sm_count();
+  const double passes = double(c.B) * c.Hkv * (((long long)(c.H / c.Hkv) * c.Sq + 15) / 16);
+  const double tiles = double(c.B) * c.H * ((c.Sq + 127) / 128);
+  const double split = passes * 4 * c.D / 7.8e6;
+  const double waves = tiles <= sms ? 1.65 : 2.4 * std::ceil(tiles / (2 * sms));
+  return waves / 128 < split;
+}
+
 }  // namespace
 
 extern "C" {
@@ -125,7 +141,11 @@ int cpattn_window_decode(const void* q, const void* k_cache, const void* v_cache
   if (S_max < 1) return CPATTN_ERR_SHAPE;
   if (sinks > S_max) c.sinks = S_max;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(c.in_f32 ? cpattn::launch_window_f32(c, cs) : cpattn::launch_window_decode(c, cs));
+  if (c.in_f32) return cuda_status(cpattn::launch_window_f32(c, cs));
+  if (!tiles_serve(c)) return cuda_status(cpattn::launch_window_decode(c, cs));
+  int* err = cpattn::device_error_word();
+  if (err == nullptr) return CPATTN_ERR_CUDA;
+  return cuda_status(cpattn::launch_window_sm100(c, err, cs));
 }
 
 }  // extern "C"

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_wait();
   griddep_release();
   const int len = sequence_length(c, b);
-  const int off = c.off;
+  const int off = c.from_end ? len - c.Sq : c.off;
   const int last_row = min(q_first + kBlockM, c.Sq) - 1;
   const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len);
   // The first loads go out before the block meets: nothing waits on their barriers earlier, and

@@ -335,6 +335,18 @@ def test_decode_strided_cache():
     check(out, lse, ow.decode_attention(qs, k, v, D ** -0.5, [777, 400], 300, 4), qs, k, D ** -0.5)
 
 
+@pytest.mark.parametrize("B,H,Hkv,Sq,S,D", [(4, 32, 8, 50, 600, 128), (9, 24, 24, 40, 300, 64), (2, 40, 8, 130, 500, 128)])
+def test_decode_of_many_tokens(B, H, Hkv, Sq, S, D):
+    # enough (token, head) rows for the tensor-core kernel, the lengths still on the device
+    q, k, v = make(24, B, H, Hkv, Sq, S, D)
+    kv_len = [S, 20, 0, Sq, 77, 299, 150, 41, 39][:B]
+    for b, n in enumerate(kv_len):
+        k[b, n:] = float("nan")
+        v[b, n:] = float("inf")
+    run_decode(q, k, v, kv_len, left=100, sinks=5)
+    run_decode(q, k, v, kv_len, left=-1, out_dtype=torch.float32)
+
+
 def test_decode_f32():
     q, k, v = make(14, 2, 4, 2, 2, 90, 48, dtype=torch.float32)
     run_decode(q, k, v, [90, 33], left=40, sinks=2)
