@@ -8,14 +8,11 @@ maximum *relative* error over f in [-1/2, 1/2] (a linear program over a dense gr
 discrete minimax fit), then are rounded to float32 and the error is re-measured with
 float32 Horner arithmetic.
 
-Run: ``python gen_exp2_poly.py [degree]`` -- prints the coefficients (decimal and hex) and the
-measured relative error bound; the kernels' constants are copied from this output (degree 3,
-the default, in sm100_ptx.cuh; degree 4 in window_sm100.cu).
+Run: ``python gen_exp2_poly.py`` -- prints the coefficients (decimal and hex) and the
+measured relative error bound; the kernel's constants are copied from this output.
 """
 
 from __future__ import annotations
-
-import sys
 
 import numpy as np
 from scipy.optimize import linprog
@@ -47,8 +44,8 @@ def horner_f32(coef32, f32):
     return np.float32(acc * f32 + np.float32(1.0)).astype(np.float32)
 
 
-def main(degree: int = 3):
-    coef, t = fit(degree)
+def main():
+    coef, t = fit()
     c32 = np.asarray(coef, dtype=np.float32)
     f = np.linspace(-0.5, 0.5, 200001, dtype=np.float32)
     p = horner_f32(c32, f)
@@ -60,4 +57,4 @@ def main(degree: int = 3):
 
 
 if __name__ == "__main__":
-    main(*(int(a) for a in sys.argv[1:2]))
+    main()

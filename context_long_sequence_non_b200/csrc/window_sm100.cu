@@ -1,41 +1,45 @@
 // window_sm100.cu -- windowed attention on B200 tensor cores (tcgen05 + TMEM + TMA), bf16 in.
 //
 // For every (b, h, query row i) at position p the softmax runs over the keys of two ranges, the
-// early (sink) keys [0, early) and the window [lo, hi) (window.h), streamed over 128-key blocks:
+// early (sink) keys [0, early) and the window [lo, hi) (window.h), streamed over 64-key blocks:
 //   S = Q K^T,  x = S scale log2(e),  m' = max(m, x),  O' = O 2^(m - m') + 2^(x - m') V,
 // with the same base-2 online softmax and reference-max rule as attn_sm100.cu: a row's reference
 // moves only when a key above it could carry 1/kMinorWeightInv of the row or exceeds it by
 // rescale_log2, so that most blocks rescale nothing.
 //
 // One CTA takes 128 query rows of one (b, h) and two CTAs share an SM.  Windows are short -- ten
-// to forty blocks -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue would
-// be a large share of its life if nothing ran beside them; with two independent CTAs one's
+// to forty blocks of 128 -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue
+// would be a large share of its life if nothing ran beside them; with two independent CTAs one's
 // softmax, start and end overlap the other's matrix products, and a tile visits its own key
 // blocks and no neighbour's.  The price, K and V not shared between two query tiles, is L2
-// traffic of 64 KB per 128 x 128 block, under half of what L2 delivers.  Blocks start at the
-// first key that the tile sees, not at a multiple of 128: a window of 4096 costs 33 blocks.
+// traffic of 64 KB per 128 x 128 products, under half of what L2 delivers.  Blocks start at the
+// first key that the tile sees, not at a multiple of 64: a window of 4096 costs 66 of them.
 //   warps 0-3  softmax, one thread per query row = TMEM lane
-//   warp  4    TMA producer: Q, then per block K (one ring) and V in two 64-key halves (another);
-//              the first loads leave before the CTA's warps have met
+//   warp  4    TMA producer: Q, then per block K into one ring and V into another; the first
+//              loads leave before the CTA's warps have met
 //   warp  5    TMEM allocator; clears V rows that no row of the tile sees (below); one of its
 //              threads issues every tcgen05.mma
-// TMEM (256 columns): S (128 fp32; P written back over it as bf16 pairs) | O (D fp32).
+// TMEM (256 columns): two S buffers of 64 fp32 (P written back over them as bf16 pairs) | O (D
+// fp32).  With two, S of block j + 1 is computed while the softmax of block j runs, and only P V
+// stands between a handoff and the S after next.  One buffer of 128 keys, S behind P V, took 3 to 8%
+// longer on every case although its products are wider (N = 64 runs at about 70% of the N = 128
+// rate): each block then paid a wake-up, P V and Q K^T between two softmaxes.
 // The bf16 epilogue leaves through shared memory and one TMA store a tile.
 //
-// What bounds it.  A block costs a CTA about 3300 cycles with its neighbour running: softmax 1900
-// (exponentials on the special-function unit and the packed FMAs around them), P V and the next
-// Q K^T 700 to 1000, wake-ups 500; the tensor pipe is busy 61% of them.  At the large sizes the
-// card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x 16 heads, causal
-// window 4096 with 64 sinks, 1.52 ms = 945 TFLOP/s of visible products; 4608 x 24, 512 to either
-// side with 512 sinks, 104 us = 760 TFLOP/s.  Tried and not kept, same cases: two 128-row tiles
-// in one CTA with shared K and V, one CTA per item (1.55 ms, 109 us; 40% slower at 333 rows) and
-// persistent over items (1.80 ms); D = 64 with P in TMEM of its own, so that S runs ahead (no
-// change); 1, 3 or 4 of every 8 exponential pairs on the FMA pipe (-1 to 0, +2, +4% time).
+// What bounds it.  64 keys cost a softmax warp 1475 cycles with its neighbour on the same scheduler:
+// 850 in the exponentials (512 of them the special-function unit's), 220 from S to the row maximum,
+// 100 for P's stores, 300 to the next S; the tensor pipe is busy about 60% of the time.  Moving a
+// share of the exponentials to the FMA pipe (1, 2 or 3 of 8, a polynomial) changes nothing.  At the
+// large sizes the card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x
+// 16 heads, causal window 4096 with 64 sinks, 1.42 ms = 1010 TFLOP/s of visible products;
+// 4608 x 24, 512 to either side with 512 sinks, 100 us = 790 TFLOP/s.  Tried and not kept, on the
+// 128-key form: two 128-row tiles in one CTA with shared K and V, one CTA per item (2% slower on
+// the first case, 40% at 333 rows) and persistent over items (19% slower).
 //
-// Hidden keys.  A block is masked per element only where some row of the warp does not see all
-// of it.  A hidden key's weight is exactly 0 or, on the polynomial's clamp, at most 2^-125 of a
-// weight of 1; 0 x NaN is NaN, though, so V rows that no row of the tile sees (past a
-// sequence's length, outside the window) are cleared in shared memory before the product.
+// Hidden keys.  A block is masked per element only where some row of the tile does not see all of
+// it, and a hidden key's weight is exactly 0.  0 x NaN is NaN, though, so V rows that no row of the
+// tile sees (past a sequence's length, outside the window) are cleared in shared memory before the
+// product.
 // Every wait is bounded (mbar_wait): a stalled pipeline sets the device error word and the CTA
 // drains and exits.
 #include <cuda_runtime.h>
@@ -49,7 +53,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kBlockM = 128;
-constexpr int kBlockN = 128;
+constexpr int kBlockN = 64;
 // Six warps: two CTAs per SM then have 168 registers a thread, which holds a row's 128 logits
 // (a 224-thread CTA would have 144, a 256-thread one 128).
 constexpr int kThreads = 192;
@@ -57,57 +61,35 @@ constexpr int kWarpProducer = 4, kWarpMma = 5;
 constexpr uint32_t kTmemCols = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kPolyPairs = 2;        // of every 8 pairs of exponentials, on the FMA pipe
 constexpr int kMinorWeightInv = 8;   // see attn_sm100.cu
-constexpr int kHalf = kBlockN / 2;   // keys of a V half and of a P handoff
-constexpr int kHalfPairs = kHalf / 2;
+constexpr int kPairs = kBlockN / 2;
 
 template <int D>
 struct Geometry {
   static constexpr int kBoxes = D / 64;                 // 64-column (128-byte) boxes per row
-  static constexpr int kBoxBytes = kBlockN * 128;       // a box of 128 rows
-  static constexpr int kVBoxBytes = kHalf * 128;        // a box of 64 rows
-  static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kVBytes = kBoxes * kVBoxBytes;
-  // K blocks and V halves in flight: what two CTAs per SM leave room for
-  static constexpr int kK = D == 128 ? 1 : 2;
-  static constexpr int kV = D == 128 ? 2 : 4;
-  static constexpr int kOffK = kTileBytes;
+  static constexpr int kQBoxBytes = kBlockM * 128;      // a box of 128 query rows
+  static constexpr int kBoxBytes = kBlockN * 128;       // a box of 64 keys
+  static constexpr int kQBytes = kBoxes * kQBoxBytes;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes; // K or V of a block
+  // K and V blocks in flight: what two CTAs per SM leave room for
+  static constexpr int kK = D == 128 ? 2 : 4;
+  static constexpr int kV = D == 128 ? 3 : 4;
+  static constexpr int kOffK = kQBytes;
   static constexpr int kOffV = kOffK + kK * kTileBytes;
-  static constexpr int kOffBars = kOffV + kV * kVBytes;
+  static constexpr int kOffBars = kOffV + kV * kTileBytes;
   static constexpr int kSmem = kOffBars + 256;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 struct __align__(8) Barriers {
-  uint64_t q_full, s_full, o_full, drain;
-  uint64_t p_part[2];  // P of keys 0..63 / 64..127 stored (the first: O rescaled too)
-  uint64_t k_full[2], k_empty[2];
+  uint64_t q_full, o_full, drain, pv_done;
+  uint64_t s_full[2], p_full[2];  // of the S buffer that block j uses, j & 1
+  uint64_t k_full[4], k_empty[4];
   uint64_t v_full[4], v_empty[4];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Barriers) <= 256, "barrier block");
-
-// 2^t for a pair of t <= 8 on the FMA pipe: Cody-Waite reduction and a degree-4 polynomial with
-// constant term 1 (gen_exp2_poly.py 4, max relative error 2.9e-6 in fp32: a quarter of the
-// weights carry it, and LSE in fp32 keeps six digits).  Clamped at -125.
-__device__ __forceinline__ float2 exp2_poly4(float2 t) {
-  constexpr float kShift = 12582912.0f;
-  constexpr float kC1 = 0.693124115f, kC2 = 0.240241066f, kC3 = 0.0559068285f, kC4 = 0.00958257634f;
-  t.x = fmaxf(t.x, -125.0f);
-  t.y = fmaxf(t.y, -125.0f);
-  const float2 j = fadd2(t, make_float2(kShift, kShift));
-  const float2 n = fadd2(j, make_float2(-kShift, -kShift));
-  const float2 f = fsub2(t, n);
-  float2 p = ffma2(f, make_float2(kC4, kC4), make_float2(kC3, kC3));
-  p = ffma2(p, f, make_float2(kC2, kC2));
-  p = ffma2(p, f, make_float2(kC1, kC1));
-  p = ffma2(p, f, make_float2(1.0f, 1.0f));
-  const uint32_t ex = __float_as_uint(j.x) << 23, ey = __float_as_uint(j.y) << 23;
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + ex),
-                     __uint_as_float(__float_as_uint(p.y) + ey));
-}
 
 // The key blocks of one tile: n_early blocks from key 0, then blocks from key w0.
 struct Blocks {
@@ -183,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarpProducer) {
     if (lane == 0) {
       mbar_init(smem_u32(&bars.q_full), 1);
-      mbar_init(smem_u32(&bars.s_full), 1);
       mbar_init(smem_u32(&bars.o_full), 1);
       mbar_init(smem_u32(&bars.drain), 1);
+      mbar_init(smem_u32(&bars.pv_done), 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&bars.p_part[i]), 4);  // one arrive per softmax warp
-        mbar_init(smem_u32(&bars.k_full[i]), 1);
-        mbar_init(smem_u32(&bars.k_empty[i]), 1);
+        mbar_init(smem_u32(&bars.s_full[i]), 1);
+        mbar_init(smem_u32(&bars.p_full[i]), 4);  // one arrive per softmax warp
       }
       for (int i = 0; i < 4; ++i) {
+        mbar_init(smem_u32(&bars.k_full[i]), 1);
+        mbar_init(smem_u32(&bars.k_empty[i]), 1);
         mbar_init(smem_u32(&bars.v_full[i]), 1);
         mbar_init(smem_u32(&bars.v_empty[i]), 1);
       }
@@ -215,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarpProducer && blk.n > 0 && lane == 0) {
     const uint32_t bar_q = smem_u32(&bars.q_full), bar_k = smem_u32(&bars.k_full[0]);
     mbar_arrive_expect_tx(bar_k, G::kTileBytes);
-    mbar_arrive_expect_tx(bar_q, G::kTileBytes);
+    mbar_arrive_expect_tx(bar_q, G::kQBytes);
 #pragma unroll
     for (int bx = 0; bx < G::kBoxes; ++bx) {
-      tma_load_4d(smem_base + bx * G::kBoxBytes, &tm_q, bar_q, bx * 64, h, q_first, b);
+      tma_load_4d(smem_base + bx * G::kQBoxBytes, &tm_q, bar_q, bx * 64, h, q_first, b);
       tma_load_4d(smem_base + G::kOffK + bx * G::kBoxBytes, &tm_k, bar_k, bx * 64, kvh, blk.base(0), b);
     }
   }
@@ -232,35 +215,41 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int row = warp * 32 + lane;
     const uint32_t lane_bits = uint32_t(warp * 32) << 16;
     const uint32_t t_s = tmem + lane_bits;
-    const uint32_t t_o = tmem + lane_bits + kBlockN;
-    const uint32_t bar_s = smem_u32(&bars.s_full);
-    const uint32_t bar_p0 = smem_u32(&bars.p_part[0]);
+    const uint32_t t_o = tmem + lane_bits + 2 * kBlockN;
+    const uint32_t bar_s0 = smem_u32(&bars.s_full[0]), bar_p0 = smem_u32(&bars.p_full[0]);
     const int q = q_first + row;
     const bool in_range = q < c.Sq;
     const KeyRange r = visible_keys(off + min(q, c.Sq - 1), c.left, c.right, c.sinks, len);
+    // keys that every row of the tile sees: blocks inside need no mask
+    const KeyRange first_row = visible_keys(off + q_first, c.left, c.right, c.sinks, len);
+    const KeyRange end_row = visible_keys(off + last_row, c.left, c.right, c.sinks, len);
+    const int full_early = min(first_row.hi, c.sinks);
+    const int full_lo = end_row.lo <= full_early ? 0 : end_row.lo, full_hi = first_row.hi;
     float m = -INFINITY;  // reference of x = s * scale * log2(e); -inf: no visible key so far
-    float l = 0.f;        // running sum of 2^(x - m)
+    // running sum of 2^(x - m), as two pairs of partial sums
+    float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
     bool ok = true;
 
     for (int j = 0; j < blk.n; ++j) {
-      ok = mbar_wait(bar_s, j & 1, abort_flag, err, wait_limit);
+      const uint32_t buf = uint32_t(j) & 1u, round = uint32_t(j >> 1) & 1u;
+      const uint32_t t_sj = t_s + buf * kBlockN;
+      ok = mbar_wait(bar_s0 + 8 * buf, round, abort_flag, err, wait_limit);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       float x[kBlockN];
       {
         uint32_t t[kBlockN];
-        tmem_ld128(t_s, t);
+        tmem_ld64(t_sj, t);
 #pragma unroll
         for (int e = 0; e < kBlockN; ++e) x[e] = __uint_as_float(t[e]);
       }
       const int kb = blk.base(j);
-      const bool sees_all = ((kb >= r.lo || r.early >= r.lo) && kb + kBlockN <= r.hi) || kb + kBlockN <= r.early;
-      if (!__all_sync(0xffffffffu, sees_all)) {
+      if (!((kb >= full_lo && kb + kBlockN <= full_hi) || kb + kBlockN <= full_early)) {
         const int early = r.early - kb, lo = r.lo - kb, hi = r.hi - kb;  // in columns of the block
         if (__any_sync(0xffffffffu, early > 0 && early < lo)) {
           // early keys, a gap, and maybe window keys: a bit per column
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < 2; ++w) {
             const uint32_t see = (low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w)) | low_bits(early - 32 * w);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -283,21 +272,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       float mx;
       {
-        float l1[44];
+        float l1[22];
 #pragma unroll
-        for (int i = 0; i < 42; ++i) l1[i] = max3(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
-        l1[42] = x[126];
-        l1[43] = x[127];
-        float l2[16];
+        for (int i = 0; i < 21; ++i) l1[i] = max3(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+        l1[21] = x[63];
+        float l2[8];
 #pragma unroll
-        for (int i = 0; i < 14; ++i) l2[i] = max3(l1[3 * i], l1[3 * i + 1], l1[3 * i + 2]);
-        l2[14] = l1[42];
-        l2[15] = l1[43];
-        float l3[6];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) l3[i] = max3(l2[3 * i], l2[3 * i + 1], l2[3 * i + 2]);
-        l3[5] = l2[15];
-        mx = fmaxf(max3(l3[0], l3[1], l3[2]), max3(l3[3], l3[4], l3[5]));
+        for (int i = 0; i < 7; ++i) l2[i] = max3(l1[3 * i], l1[3 * i + 1], l1[3 * i + 2]);
+        l2[7] = l1[21];
+        mx = fmaxf(max3(l2[0], l2[1], l2[2]), max3(max3(l2[3], l2[4], l2[5]), l2[6], l2[7]));
       }
       const float m_tile = mx * scale_log2;
       float alpha = 1.0f;
@@ -308,59 +291,51 @@ __global__ void __launch_bounds__(kThreads, 2)
         // a row that has seen no key yet (m = -inf) takes the block's maximum; its O is 0
         const float d = m_tile - m;
         bool grow = d > rescale_log2;
-        if (!grow && d > 0.f) grow = ex2(d) * float(kMinorWeightInv - 1) >= l;
+        if (!grow && d > 0.f) grow = ex2(d) * float(kMinorWeightInv - 1) >= (l0.x + l0.y) + (l1.x + l1.y);
         rescale = __any_sync(0xffffffffu, grow);
         if (rescale) {
           alpha = grow ? ex2(m - m_tile) : 1.0f;
           if (grow) m = m_tile;
-          l *= alpha;
+          l0 = fmul2(l0, make_float2(alpha, alpha));
+          l1 = fmul2(l1, make_float2(alpha, alpha));
         }
       }
       const float neg_m = m == -INFINITY ? 0.f : -m;
       const float2 sl2 = make_float2(scale_log2, scale_log2);
       const float2 nm2 = make_float2(neg_m, neg_m);
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+      uint32_t pk[kPairs];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        uint32_t pk[kHalfPairs];
-#pragma unroll
-        for (int e = 0; e < kHalfPairs; ++e) {
-          const int cc = 2 * (part * kHalfPairs + e);
-          const float2 t = ffma2(make_float2(x[cc], x[cc + 1]), sl2, nm2);
-          float2 pv;
-          if ((e & 7) >= 8 - kPolyPairs) {
-            pv = exp2_poly4(t);
-          } else {
-            pv.x = ex2(t.x);
-            pv.y = ex2(t.y);
-          }
-          if (e & 1) acc1 = fadd2(acc1, pv);
-          else acc0 = fadd2(acc0, pv);
-          pk[e] = pack_bf16x2(pv.x, pv.y);  // weights in bf16 for the product; l keeps fp32
-        }
-        tmem_st_any(t_s + part * kHalfPairs, pk);
-        if (part == 0 && rescale) {
-          const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll
-          for (int oc = 0; oc < D / 32; ++oc) {
-            uint32_t t[32];
-            tmem_ld32(t_o + oc * 32, t);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 o = fmul2(make_float2(__uint_as_float(t[e]), __uint_as_float(t[e + 1])), a2);
-              t[e] = __float_as_uint(o.x);
-              t[e + 1] = __float_as_uint(o.y);
-            }
-            tmem_st32(t_o + oc * 32, t);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p0 + 8 * part);
+      for (int e = 0; e < kPairs; ++e) {
+        const float2 t = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sl2, nm2);
+        const float2 pv = make_float2(ex2(t.x), ex2(t.y));  // 2^-inf = 0 for a hidden key
+        if (e & 1) l1 = fadd2(l1, pv);
+        else l0 = fadd2(l0, pv);
+        pk[e] = pack_bf16x2(pv.x, pv.y);  // weights in bf16 for the product; l keeps fp32
       }
-      const float2 acc = fadd2(acc0, acc1);
-      l += acc.x + acc.y;
+      tmem_st32(t_sj, pk);
+      if (rescale) {
+        // S ran ahead of the last block's P V, which must have left O before it is rescaled
+        ok = mbar_wait(smem_u32(&bars.pv_done), uint32_t(j - 1) & 1u, abort_flag, err, wait_limit);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t t[32];
+          tmem_ld32(t_o + oc * 32, t);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 o = fmul2(make_float2(__uint_as_float(t[e]), __uint_as_float(t[e + 1])), a2);
+            t[e] = __float_as_uint(o.x);
+            t[e + 1] = __float_as_uint(o.y);
+          }
+          tmem_st32(t_o + oc * 32, t);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p0 + 8 * buf);
     }
 
     // ------------------------------------------------------------------ epilogue
@@ -373,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (ok) {
       tc_fence_after();
+      const float l = (l0.x + l0.y) + (l1.x + l1.y);
       const bool empty = m == -INFINITY;
       const float lc2 = m + log2f(l);
       float fa = 0.f, fc = empty ? 0.f : 1.0f / l;
@@ -415,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                               __uint_as_float(t[8 * e + 2 * i + 1]) * fc);
             const uint32_t v = uint32_t((oc & 1) * 4 + e);  // 16-byte vector of the 64-column box
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             row_addr + uint32_t(oc >> 1) * G::kBoxBytes + ((v ^ (uint32_t(row) & 7u)) << 4)),
+                             row_addr + uint32_t(oc >> 1) * G::kQBoxBytes + ((v ^ (uint32_t(row) & 7u)) << 4)),
                          "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                          : "memory");
           }
@@ -486,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (bar_and(1, 128, ok) && threadIdx.x == 0) {
 #pragma unroll
         for (int bx = 0; bx < G::kBoxes; ++bx)
-          tma_store_4d(&tm_o, smem_base + bx * G::kBoxBytes, bx * 64, h, q_first, b);
+          tma_store_4d(&tm_o, smem_base + bx * G::kQBoxBytes, bx * 64, h, q_first, b);
         tma_store_wait();
       }
     }
@@ -495,8 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (blk.n > 0 && lane == 0) {
       const uint32_t bar_q = smem_u32(&bars.q_full);
       int k_issued = 1, v_issued = 0;  // K of block 0 and Q are on their way
-      bool go = true;
-      for (int j = 0; go && j < blk.n; ++j) {
+      for (int j = 0; j < blk.n; ++j) {
         const int kb = blk.base(j);
         const int ks = j % G::kK;
         if (j > 0) {
@@ -511,21 +486,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                         kvh, kb, b);
           k_issued = j + 1;
         }
-        for (int half = 0; half < 2; ++half) {
-          const int use = 2 * j + half, vs = use % G::kV;
-          if (!mbar_wait(smem_u32(&bars.v_empty[vs]), (uint32_t(use / G::kV) & 1u) ^ 1u, abort_flag, err,
-                         wait_limit)) {
-            go = false;
-            break;
-          }
-          const uint32_t bar_v = smem_u32(&bars.v_full[vs]);
-          mbar_arrive_expect_tx(bar_v, G::kVBytes);
+        const int vs = j % G::kV;
+        if (!mbar_wait(smem_u32(&bars.v_empty[vs]), (uint32_t(j / G::kV) & 1u) ^ 1u, abort_flag, err, wait_limit))
+          break;
+        const uint32_t bar_v = smem_u32(&bars.v_full[vs]);
+        mbar_arrive_expect_tx(bar_v, G::kTileBytes);
 #pragma unroll
-          for (int bx = 0; bx < G::kBoxes; ++bx)
-            tma_load_4d(smem_base + G::kOffV + vs * G::kVBytes + bx * G::kVBoxBytes, &tm_v, bar_v, bx * 64,
-                        kvh, kb + half * kHalf, b);
-          v_issued = use + 1;
-        }
+        for (int bx = 0; bx < G::kBoxes; ++bx)
+          tma_load_4d(smem_base + G::kOffV + vs * G::kTileBytes + bx * G::kBoxBytes, &tm_v, bar_v, bx * 64, kvh, kb, b);
+        v_issued = j + 1;
       }
       // every issued copy lands before the CTA's shared memory is released
       drain_wait(bar_q, 0, wait_limit);
@@ -544,50 +513,48 @@ __global__ void __launch_bounds__(kThreads, 2)
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, D, true);
       const uint64_t q_desc = sdesc_sw128(smem_base, 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_base + G::kOffK, 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(smem_base + G::kOffV, G::kVBoxBytes, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_base + G::kOffV, G::kBoxBytes, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return mbar_wait(smem_u32(bar), parity & 1u, abort_flag, err, wait_limit);
       };
-      // S = Q K^T over D in K = 16 steps: 32 bytes per step inside a 128-byte swizzled row, the
-      // next 64 columns in the next box
-      auto issue_qk = [&](int ks) {
+      // S = Q K^T of block j into buffer j & 1, over D in K = 16 steps: 32 bytes per step inside a
+      // 128-byte swizzled row, the next 64 columns in the next box
+      auto issue_qk = [&](int j) {
+        const int ks = j % G::kK;
+        if (!wait(&bars.k_full[ks], uint32_t(j / G::kK))) return false;
+        tc_fence_after();
         const uint64_t kd = k_desc + uint32_t(ks * (G::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * G::kBoxBytes + (kk & 3) * 32) >> 4;
-          mma_ss(tmem, q_desc + o, kd + o, idesc_qk, kk > 0 ? 1u : 0u);
+          const uint32_t qo = ((kk >> 2) * G::kQBoxBytes + (kk & 3) * 32) >> 4;
+          const uint32_t ko = ((kk >> 2) * G::kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + (j & 1) * kBlockN, q_desc + qo, kd + ko, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        tc_commit(smem_u32(&bars.s_full));
+        tc_commit(smem_u32(&bars.s_full[j & 1]));
         tc_commit(smem_u32(&bars.k_empty[ks]));
+        return true;
       };
       bool ok = true;
       if (leader) {
-        ok = wait(&bars.q_full, 0) && wait(&bars.k_full[0], 0);
-        if (ok) {
-          tc_fence_after();
-          issue_qk(0);
-        }
+        ok = wait(&bars.q_full, 0) && issue_qk(0);
+        if (blk.n > 1) ok = ok && issue_qk(1);
       }
+      int vs = 0;
+      uint32_t v_round = 0;
       for (int j = 0; j < blk.n; ++j) {
         const int kb = blk.base(j);
-        const int v0 = (2 * j) % G::kV;  // slots v0 and v0 + 1 (kV is even)
-        const uint32_t v_ph = uint32_t(2 * j / G::kV);
         const int k1 = min(kb + kBlockN, c.Skv);  // rows past Skv arrive as 0
         if (!blk.all_seen(kb, k1)) {
-          bool landed = wait(&bars.v_full[v0], v_ph) && wait(&bars.v_full[v0 + 1], v_ph);
+          bool landed = wait(&bars.v_full[vs], v_round);
           landed = __all_sync(0xffffffffu, landed);
           // the hidden rows are [early, lo) and [hi, ..) of the block: whole 128-byte rows of each
           // box, whatever the swizzle, so runs of 16-byte stores
+          uint8_t* v = smem + G::kOffV + vs * G::kTileBytes;
           auto clear = [&](int r0, int r1) {
+            for (int o = r0 * 128 + lane * 16; o < r1 * 128; o += 512)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int a = max(r0 - half * kHalf, 0) * 128, z = min(r1 - half * kHalf, kHalf) * 128;
-              uint8_t* v = smem + G::kOffV + (v0 + half) * G::kVBytes;
-              for (int o = a + lane * 16; o < z; o += 512)
-#pragma unroll
-                for (int bx = 0; bx < G::kBoxes; ++bx)
-                  *reinterpret_cast<uint4*>(v + bx * G::kVBoxBytes + o) = make_uint4(0u, 0u, 0u, 0u);
-            }
+              for (int bx = 0; bx < G::kBoxes; ++bx)
+                *reinterpret_cast<uint4*>(v + bx * G::kBoxBytes + o) = make_uint4(0u, 0u, 0u, 0u);
           };
           if (landed) {
             clear(max(blk.early - kb, 0), min(blk.lo, k1) - kb);
@@ -597,30 +564,26 @@ __global__ void __launch_bounds__(kThreads, 2)
           __syncwarp();
         }
         if (leader && ok) {
-          // everything but P is waited for first: between P's arrival and the products there is
-          // nothing but their issue
-          const bool more = j + 1 < blk.n;
-          const int ks = (j + 1) % G::kK;
-          ok = wait(&bars.v_full[v0], v_ph) && wait(&bars.v_full[v0 + 1], v_ph);
-          const uint64_t vd = v_desc + uint32_t(v0 * (G::kVBytes >> 4));
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (half == 1 && more) ok = ok && wait(&bars.k_full[ks], uint32_t((j + 1) / G::kK));
-            ok = ok && wait(&bars.p_part[half], uint32_t(j));
-            if (!ok) break;
+          ok = wait(&bars.v_full[vs], v_round) && wait(&bars.p_full[j & 1], uint32_t(j >> 1));
+          if (ok) {
             tc_fence_after();
-            // O += P V over 64 keys in K = 16 steps: P from TMEM (8 columns per step), V MN-major
+            // O += P V over the 64 keys in K = 16 steps: P from TMEM (8 columns per step), V MN-major
             // (16 key rows = 2 KB per step, the next 64 columns of D in the next box)
+            const uint64_t vd = v_desc + uint32_t(vs * (G::kTileBytes >> 4));
 #pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-              mma_ts(tmem + kBlockN, tmem + half * kHalfPairs + kk * 8,
-                     vd + uint32_t((half * G::kVBytes + kk * 16 * 128) >> 4), idesc_pv,
-                     (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(smem_u32(&bars.v_empty[v0 + half]));
+            for (int kk = 0; kk < kBlockN / 16; ++kk)
+              mma_ts(tmem + 2 * kBlockN, tmem + (j & 1) * kBlockN + kk * 8, vd + uint32_t((kk * 16 * 128) >> 4), idesc_pv,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&bars.v_empty[vs]));
+            tc_commit(smem_u32(&bars.pv_done));
+            if (j + 2 < blk.n) ok = issue_qk(j + 2);  // over P of this block, after its product
           }
-          if (ok && more) issue_qk(ks);
         }
         __syncwarp();
+        if (++vs == G::kV) {
+          vs = 0;
+          ++v_round;
+        }
       }
       if (leader) {
         if (ok) tc_commit(smem_u32(&bars.o_full));
@@ -692,7 +655,7 @@ cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stre
   if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM)) return cudaErrorInvalidValue;
   if (c.Skv == 0) tk = tv = tq;  // no block loads through them
   else if (!encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
-           !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kHalf))
+           !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kBlockN))
     return cudaErrorInvalidValue;
   // bf16 results leave by TMA; the other forms do not use the map
   if (c.out_f32 || c.accumulate) to = tq;
