@@ -17,9 +17,13 @@
 //
 // Loads.  Each warp keeps kStages chunks of 16 keys in flight with 16-byte cp.async, 192 KB per SM
 // (two CTAs of D = 128, four of D = 64), rows swizzled so that ldmatrix reads without bank
-// conflicts.  Early (sink) keys and window keys form one list, so no chunk is
-// spent on a boundary; rows that no query sees are never read, and the list's end is filled
-// with zeros.
+// conflicts.  Early (sink) keys and window keys form one list, so no chunk is spent on a boundary;
+// rows that no query sees are never read, and the list's end is filled with zeros.
+//
+// Measured on a B200: 64 sequences x 32 heads on 8, 4100 keys at most, 122 us = 6.0 TB/s of K and V
+// (92% of the measured copy rate; ncu counts 740 MB, the visible rows once); one sequence x 32 on 8
+// over 1028 keys 5.5 us, all of it latency: two launches' overlap, one read, the fold; 8 sequences
+// x 16 heads of 64, 4 tokens each, 12 to 13 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -112,7 +116,6 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
   const int n_rows = min(kRows, G * c.Sq - row0);
 
   griddep_wait();
-  griddep_release();
 
   const int len = sequence_length(c, b);
   const int off = len - c.Sq;
@@ -265,6 +268,9 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
     __syncwarp();  // the stage is read before it is refilled
   }
   cp_async_wait<0>();
+  // The next launch's blocks may take the places this one leaves from here on; let in at the start,
+  // they crowded some SMs (8 sequences of 4 tokens, calls back to back: 15.1 us against 13.3).
+  griddep_release();
 
   // ---- fold the warps' partials: m and l first, then O scaled to the block's maximum
 #pragma unroll
