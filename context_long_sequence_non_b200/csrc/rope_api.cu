@@ -50,7 +50,8 @@ int check(RopeCall* c, int dtype, bool scattered) {
     if (t.src_stride == 0) t.src_stride = row;
     if (t.dst_stride == 0) t.dst_stride = row;
     if (t.src_stride < row || (!scattered && t.dst_stride < row)) return CPATTN_ERR_SHAPE;
-    if (t.src_stride > (1LL << 36) || t.dst_stride > (1LL << 36)) return CPATTN_ERR_SHAPE;
+    // 2^31 tokens less than 2^30 elements apart: every extent below fits 64 bits
+    if (t.src_stride >= (1LL << 30) || t.dst_stride >= (1LL << 30)) return CPATTN_ERR_SHAPE;
   }
   if (c->tokens == 0) return CPATTN_OK;  // nothing is read or written: pointers are not checked
   if (c->pos_rows < 1 || c->tokens % c->pos_rows != 0) return CPATTN_ERR_SHAPE;

@@ -20,9 +20,12 @@ constexpr int kMaxPos = 1 << 30;  // positions stay below this, so position arit
 
 int clamp_extent(int n) { return n < 0 ? -1 : (n >= kMaxPos ? kMaxPos - 1 : n); }
 
-// Bytes from the first to the last element of n tokens of `row` elements each, `stride` apart.
+// Bytes from the first to the last element of n tokens of `row` elements each, `stride` apart (at
+// most 2^30 tokens a batch, less than 2^40 bytes apart: capped where that passes any memory).
 size_t span_bytes(long long tokens, long long stride, long long row, int es) {
-  return tokens < 1 ? 0 : size_t((tokens - 1) * stride + row) * es;
+  if (tokens < 1) return 0;
+  const double bytes = (double(tokens - 1) * double(stride) + double(row)) * es;
+  return bytes > 1e18 ? size_t(1) << 60 : size_t((tokens - 1) * stride + row) * es;
 }
 
 // Checks shared by both calls; fills the strides in (0: packed).
@@ -41,13 +44,11 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
   if (c->q_stride == 0) c->q_stride = q_row;
   if (c->k_stride == 0) c->k_stride = kv_row;
   if (c->v_stride == 0) c->v_stride = kv_row;
-  const long long most = 1LL << 36;  // elements: 2^37 bytes, inside a tensor map's 40-bit stride
-  if (c->q_stride < q_row || c->k_stride < kv_row || c->v_stride < kv_row || c->q_stride > most ||
-      c->k_stride > most || c->v_stride > most)
-    return CPATTN_ERR_SHAPE;
-  // batches are less than 2^40 bytes apart (a tensor map's limit)
-  if (c->B > 1 && (c->Sq * c->q_stride * es >> 40 || c->Skv * c->k_stride * es >> 40 ||
-                   c->Skv * c->v_stride * es >> 40))
+  if (c->q_stride < q_row || c->k_stride < kv_row || c->v_stride < kv_row) return CPATTN_ERR_SHAPE;
+  // a tensor map's strides are below 2^40 bytes, from token to token and from batch to batch
+  const int q_steps = c->B > 1 ? c->Sq : 1, kv_steps = c->B > 1 && c->Skv > 1 ? c->Skv : 1;
+  const long long most = (1LL << 40) / es - 1;
+  if (c->q_stride > most / q_steps || c->k_stride > most / kv_steps || c->v_stride > most / kv_steps)
     return CPATTN_ERR_SHAPE;
   if (c->q == nullptr || c->out == nullptr || (c->accumulate && c->lse == nullptr)) return CPATTN_ERR_NULL;
   if (c->Skv > 0 && (c->k == nullptr || c->v == nullptr)) return CPATTN_ERR_NULL;

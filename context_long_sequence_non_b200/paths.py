@@ -46,6 +46,9 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
     if left >= 0 or right >= 0:
         if not fused or n_split != 1:
             raise ValueError("a windowed ring step is fused and not split")
+        if len(k_chunks) < 1 or len(v_chunks) != len(k_chunks) or (
+                k_pos is not None and len(k_pos) != len(k_chunks)):
+            raise ValueError("a windowed ring step needs chunks, and a position for each")
         if k_pos is None:
             k_pos, at = [], 0
             for kc in k_chunks:

@@ -384,8 +384,8 @@ CPATTN_API int cpattn_head2seq(const void* src, void* dst, int P, int S_local, i
  * q : [B][Sq][H][D], k and v : [B][Skv][Hkv][D], H a multiple of Hkv: query head h uses key head
  *   h / (H / Hkv).  q_stride, k_stride, v_stride: elements between consecutive tokens, 0 for
  *   packed rows (H*D or Hkv*D); a larger stride takes heads out of a wider row, such as one
- *   projection's output.  Consecutive batches are Sq (Skv) such tokens apart.  bf16 strides are
- *   multiples of 8 (CPATTN_ERR_ALIGN).
+ *   projection's output.  Consecutive batches are Sq (Skv) such tokens apart, less than 2^40
+ *   bytes.  bf16 strides are multiples of 8 (CPATTN_ERR_ALIGN).
  * out : [B][Sq][H][D] packed, lse : [B][H][Sq] float32, or NULL to skip it.
  * kv_len : B ints in device memory, or NULL.  Rows of k and v at or past the length are never
  *   used, whatever they hold (NaN included), and neither are rows that no query of the call
@@ -459,7 +459,8 @@ CPATTN_API int cpattn_rope_frequencies(double* freq, float* factor, int rot, dou
  * undoes one.  Several axes (frame, row, column of a video token) each turn the pairs whose
  * freq[a][p] is not 0.
  * x, y : [tokens][H][D] in `dtype` (BF16 or F32), x_stride / y_stride elements between tokens
- *   (0: packed, H*D); y may be x itself with the same stride, and must not overlap it otherwise.
+ *   (0: packed, H*D; below 2^30); y may be x itself with the same stride, and must not overlap
+ *   it otherwise.
  * pos : [pos_rows][n_axes] int32, freq : [n_axes][rot/2] double, both in device memory; tokens a
  *   multiple of pos_rows (a batch of sequences at the same positions gives pos_rows = their
  *   length).  2 <= rot <= D <= 256, rot even; 1 <= n_axes <= 4; tokens >= 0 (0 is a no-op that

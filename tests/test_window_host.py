@@ -65,6 +65,10 @@ def test_window_argument_errors(L, call):
     assert call(L, qs=511) == B.ERR_SHAPE  # shorter than a token's heads
     assert call(L, ks=255) == B.ERR_SHAPE
     assert call(L, vs=1 << 40) == B.ERR_SHAPE
+    for big in (1 << 39, 1 << 62):  # batches or tokens too far apart
+        assert call(L, ks=big) == B.ERR_SHAPE
+        assert call(L, qs=big, B_=2, Sq=3) == B.ERR_SHAPE
+    assert call(L, vs=1 << 38, B_=2) == B.ERR_SHAPE
     assert call(L, qs=516) == B.ERR_ALIGN  # bf16 rows start on 16 bytes
     assert call(L, o=FAKE) == B.ERR_SHAPE  # out over q
     assert call(L, o=FAKE + BIG + 16) == B.ERR_SHAPE  # out over k
@@ -115,6 +119,8 @@ def test_rope_argument_errors(L):
     assert rope(L, T=1 << 30, H=4) == B.ERR_SHAPE
     assert rope(L, xs=255) == B.ERR_SHAPE
     assert rope(L, ys=255) == B.ERR_SHAPE
+    assert rope(L, xs=1 << 30) == B.ERR_SHAPE
+    assert rope(L, ys=1 << 62) == B.ERR_SHAPE
     assert rope(L, x=None) == B.ERR_NULL
     assert rope(L, y=None) == B.ERR_NULL
     assert rope(L, pos=None) == B.ERR_NULL
@@ -282,3 +288,7 @@ def test_rope_binding_checks():
         cp.seq2head_qkv_norm_rope(s, s, s, 2, g, g, torch.zeros(5, dtype=torch.int32), f)
     with pytest.raises(ValueError, match="ring step"):
         cp.ring_attention(s, [s], [s], left=3, fused=False)
+    with pytest.raises(ValueError, match="needs chunks"):
+        cp.ring_attention(s, [], [], left=3)
+    with pytest.raises(ValueError, match="needs chunks"):
+        cp.ring_attention(s, [s], [s], left=3, k_pos=[0, 5])
