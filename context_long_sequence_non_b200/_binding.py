@@ -439,7 +439,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(index, stream, what, fn, *args):
+def _call(index, stream, what, fn, args):
     """Run a library call with CUDA device ``index`` current (the library launches on the current
     device) on ``stream``, or on that device's current stream."""
     if stream is None:
@@ -459,9 +459,9 @@ def _call(index, stream, what, fn, *args):
 
 def _same_device(first, *ts):
     """The CUDA device index that every tensor is on."""
-    if not first.is_cuda:
+    index = first.get_device()  # -1: not a CUDA tensor
+    if index < 0:
         raise ValueError("tensors must live on a CUDA device")
-    index = first.get_device()
     for t in ts:
         if t is not None and t.get_device() != index:
             raise ValueError("tensors must live on one CUDA device")
@@ -502,38 +502,46 @@ def _packed(t, shape, name, dtype):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _extent(n, name, least=-(1 << 31)):
+def _extent(n, name):
     n = int(n)
-    if not least <= n < 1 << 31:
+    if not -(1 << 31) <= n < 1 << 31:
         raise ValueError(f"{name} is out of range")
     return n
 
 
+_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
 def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
-    kv_shape, dtype = k.shape, q.dtype
-    if q.dim() != 4 or len(kv_shape) != 4:
+    q_shape, kv_shape, dtype = q.shape, k.shape, q.dtype
+    if len(q_shape) != 4 or len(kv_shape) != 4:
         raise ValueError("q, k and v must be [B][S][H][D]")
-    B, Sq, H, D = q.shape
+    B, Sq, H, D = q_shape
     Bk, Skv, Hkv, Dk = kv_shape
     if Bk != B or Dk != D or v.shape != kv_shape:
         raise ValueError("k and v must be [B][Skv][Hkv][D] matching q")
     if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("q, k and v must have one dtype")
-    strides = (_token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
+    # 0: packed tokens
+    qs = 0 if q.is_contiguous() else _token_stride(q, "q")
+    ks = 0 if k.is_contiguous() else _token_stride(k, "k")
+    vs = 0 if v.is_contiguous() else _token_stride(v, "v")
     if kv_len is not None:
         _packed(kv_len, (B,), "kv_len", torch.int32)
     if out is None:
-        out = torch.empty((B, Sq, H, D), dtype=out_dtype or dtype, device=q.device)
+        out = torch.empty(q_shape, dtype=out_dtype or dtype, device=q.device)
     else:
-        _packed(out, (B, Sq, H, D), "out", out_dtype)
+        _packed(out, q_shape, "out", out_dtype)
     if lse is not None:
         _packed(lse, (B, H, Sq), "lse", torch.float32)
     elif want_lse:
         lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
     index = _same_device(q, k, v, kv_len, out, lse)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    return index, (B, H, Hkv, Sq, Skv, D) + strides, float(scale), out, lse
+    codes = _CODE.get(dtype), _CODE.get(out.dtype)
+    if None in codes:
+        raise TypeError(f"unsupported dtype {dtype if codes[0] is None else out.dtype}")
+    return (index, (B, H, Hkv, Sq, Skv, D, qs, ks, vs, 1.0 / math.sqrt(D) if scale is None else float(scale)),
+            codes, out, lse)
 
 
 def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=None, out=None,
@@ -545,22 +553,23 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
     q: [B][Sq][H][D], k/v: [B][Skv][Hkv][D] with H a multiple of Hkv (bf16 -> tensor-core kernel,
     D 64 or 128; fp32 -> CUDA-core kernel, D <= 256); their heads may be slices of a wider row.
     ``kv_len``: int32 [B], keys of each sequence.  ``accumulate`` merges into the running
-    (out, lse), or merges the running (``run`` float32, lse) into a bf16 ``out``.  Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
+    (out, lse), or merges the running (``run`` float32, lse) into a bf16 ``out``.
+    Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
     if accumulate and (lse is None or (out is None and run is None)):
         raise ValueError("accumulate needs the running out and lse")
     if run is not None:
         if not accumulate:
             raise ValueError("run is the running result of an accumulating call")
         _packed(run, q.shape, "run", torch.float32)
-    index, dims, scale, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
+    index, dims, codes, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
     if run is not None:
         _same_device(q, run)
-    _call(index, stream, "cpattn_window_fwd", lib().cpattn_window_fwd, q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-          None if kv_len is None else kv_len.data_ptr(), None if run is None else run.data_ptr(), *dims,
-          scale, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
-          _extent(left, "left"), _extent(right, "right"), _extent(sinks, "sinks"),
-          _dtype_code(q.dtype), _dtype_code(out.dtype), 1 if accumulate else 0)
+    _call(index, stream, "cpattn_window_fwd", lib().cpattn_window_fwd,
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+           None if lse is None else lse.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
+           None if run is None else run.data_ptr(), *dims, _extent(q_pos, "q_pos"),
+           _extent(k_pos, "k_pos"), _extent(left, "left"), _extent(right, "right"),
+           _extent(sinks, "sinks"), *codes, 1 if accumulate else 0))
     return out, lse
 
 
@@ -569,12 +578,13 @@ def window_decode(q, k_cache, v_cache, kv_len=None, left=-1, sinks=0, out=None, 
     """The last Sq tokens of each sequence against its cache (causal, window and sinks as
     window_fwd): q [B][Sq][H][D], caches [B][S_max][Hkv][D], ``kv_len`` int32 [B] the tokens each
     sequence holds, the newest included (None: S_max).  See cpattn_window_decode."""
-    index, dims, scale, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale, out_dtype,
+    index, dims, codes, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale, out_dtype,
                                                 want_lse)
-    _call(index, stream, "cpattn_window_decode", lib().cpattn_window_decode, q.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
-          out.data_ptr(), None if lse is None else lse.data_ptr(), *dims, scale, _extent(left, "left"),
-          _extent(sinks, "sinks"), _dtype_code(q.dtype), _dtype_code(out.dtype))
+    _call(index, stream, "cpattn_window_decode", lib().cpattn_window_decode,
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+           None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
+           None if lse is None else lse.data_ptr(), *dims, _extent(left, "left"),
+           _extent(sinks, "sinks"), *codes))
     return out, lse
 
 
@@ -641,9 +651,10 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
     elif out.shape != shape or out.dtype != dtype:
         _need_shape(out, shape, "out", dtype)
     index = _same_device(x, pos, freq, out)
-    _call(index, stream, "cpattn_rope", lib().cpattn_rope, x.data_ptr(), out.data_ptr(),
-          pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes, 1 if interleaved else 0,
-          float(factor), _token_stride(x, "x"), _token_stride(out, "out"), _dtype_code(dtype))
+    _call(index, stream, "cpattn_rope", lib().cpattn_rope,
+          (x.data_ptr(), out.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes,
+           1 if interleaved else 0, float(factor), _token_stride(x, "x"), _token_stride(out, "out"),
+           _dtype_code(dtype)))
     return out
 
 
@@ -666,12 +677,12 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.
     _need_shape(qo, q.shape, "out[0]", q.dtype)
     _need_shape(ko, k.shape, "out[1]", k.dtype)
     index = _same_device(q, k, gamma_q, gamma_k, pos, freq, qo, ko)
-    _call(index, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope, q.data_ptr(),
-          k.data_ptr(), qo.data_ptr(), ko.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(),
-          pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2], k.shape[-2], D, rot, axes,
-          1 if interleaved else 0, float(eps), float(out_scale), float(factor),
-          _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(qo, "out[0]"),
-          _token_stride(ko, "out[1]"), _dtype_code(q.dtype))
+    _call(index, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope,
+          (q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(), gamma_q.data_ptr(),
+           gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2], k.shape[-2],
+           D, rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor),
+           _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(qo, "out[0]"),
+           _token_stride(ko, "out[1]"), _dtype_code(q.dtype)))
     return qo, ko
 
 
@@ -702,10 +713,10 @@ def seq2head_qkv_norm_rope(q, k, v, P, gamma_q, gamma_k, pos, freq, interleaved=
             raise ValueError("q, k, v must be contiguous")
     index = _same_device(q, k, v, gamma_q, gamma_k, pos, freq, *out)
     _call(index, stream, "cpattn_seq2head_qkv_norm_rope", lib().cpattn_seq2head_qkv_norm_rope,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out),
-          None if gamma_q is None else gamma_q.data_ptr(),
-          None if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H,
-          D, rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor))
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out),
+           None if gamma_q is None else gamma_q.data_ptr(),
+           None if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H, D,
+           rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor)))
     return out
 
 
