@@ -155,10 +155,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t smem_base = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // CTAs run in index order, x fastest, so the tiles with the most keys (the last ones, when the
-  // window grows with the position) come first within each head and the grid ends on short ones
-  const int tile = int(gridDim.x) - 1 - int(blockIdx.x);
-  const int h = blockIdx.y, b = blockIdx.z;
+  // CTAs run in index order: the tiles with the most keys (the last ones, when the window grows with
+  // the position) come first, those of all heads beside one another, so that the grid as a whole ends
+  // on short ones.  Head by head instead it ends on the last head's full range: causal 8192 x 16 heads
+  // 302 us against 264, a ring step's 5520 rows x 16 heads in 3 parts 385 against 357, 4608 x 24 103
+  // against 100; 44160 x 16, where a head alone fills the GPU, 1450 against 1462
+  const unsigned n_heads = unsigned(c.H) * unsigned(c.B);
+  const int tile = int((gridDim.x - 1 - blockIdx.x) / n_heads);
+  const int bh = int(blockIdx.x % n_heads);
+  const int b = bh / c.H, h = bh - b * c.H;
   const int q_first = tile * kBlockM;
   volatile int* abort_flag = &bars.abort;
 
@@ -623,7 +628,7 @@ cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM), unsigned(c.H), unsigned(c.B));
+  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM) * unsigned(c.H) * unsigned(c.B));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Geometry<D>::kSmem;
   cfg.stream = stream;
