@@ -184,6 +184,26 @@ def test_f32_many_rows(D):
     run_window(q, k, v, left=40, right=9, sinks=3)
 
 
+@pytest.mark.parametrize("D", [64, 100, 128])
+def test_f32_enough_rows_for_the_widest_tiles(D):
+    q, k, v = make(25, 2, 8, 2, 1400, 1400, D, dtype=torch.float32)  # 468 blocks of 48 (token, head) rows
+    run_window(q, k, v, left=40, right=9, sinks=3)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Sq,Skv,D", [(1, 1, 1, 20, 1500, 128), (1, 2, 1, 40, 700, 64), (2, 2, 2, 33, 300, 256),
+                                              (1, 3, 3, 100, 2000, 64), (1, 6, 2, 7, 130, 33), (1, 7, 1, 1, 65, 128),
+                                              (1, 12, 4, 300, 65, 64)])
+@pytest.mark.parametrize("w", [dict(left=-1, right=-1), dict(left=-1, right=0), dict(left=150, right=0, sinks=70)])
+def test_f32_keys_shared_out_to_a_cluster(B, H, Hkv, Sq, Skv, D, w):
+    q, k, v = make(26 + D, B, H, Hkv, Sq, Skv, D, dtype=torch.float32)
+    o, l = run_window(q, k, v, q_pos=max(Skv - Sq, 0), **w)
+    again = run_window(q, k, v, q_pos=max(Skv - Sq, 0), **w)
+    assert torch.equal(o, again[0]) and torch.equal(l, again[1])  # a fixed order of sums
+    # blocks whose share of the keys is empty, and rows that see nothing
+    run_window(q, k, v, kv_len=[Skv // 7] * B, q_pos=max(Skv - Sq, 0), out_dtype=torch.bfloat16, **w)
+    run_window(q, k, v, kv_len=[Skv] + [0] * (B - 1), k_pos=Sq // 2, **w)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_calls(seed):
     r = np.random.default_rng(1000 + seed)
@@ -350,6 +370,34 @@ def test_decode_of_many_tokens(B, H, Hkv, Sq, S, D):
 def test_decode_f32():
     q, k, v = make(14, 2, 4, 2, 2, 90, 48, dtype=torch.float32)
     run_decode(q, k, v, [90, 33], left=40, sinks=2)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Sq,S,D", [(1, 8, 8, 1, 3000, 128), (3, 8, 2, 1, 700, 64), (2, 16, 1, 1, 333, 256),
+                                            (1, 40, 2, 3, 260, 64), (5, 3, 3, 17, 129, 48), (2, 5, 1, 1, 1, 7),
+                                            (4, 32, 8, 2, 513, 128), (70, 10, 5, 1, 40, 64)])
+@pytest.mark.parametrize("w", [dict(left=-1), dict(left=0), dict(left=100, sinks=4)])
+def test_decode_f32_forms(B, H, Hkv, Sq, S, D, w):
+    q, k, v = make(B + H + D, B, H, Hkv, Sq, S, D, dtype=torch.float32)
+    r = np.random.default_rng(S)
+    kv_len = [S] + [int(x) for x in r.integers(0, S + 1, B - 1)]
+    for b, n in enumerate(kv_len):
+        k[b, n:] = float("nan")
+        v[b, n:] = float("inf")
+    run_decode(q, k, v, kv_len, **w)
+    run_decode(q, k, v, kv_len, out_dtype=torch.bfloat16, **w)
+
+
+def test_decode_f32_strided_cache():
+    B, S, Hkv, D = 2, 777, 2, 64
+    g = torch.Generator().manual_seed(27)
+    kv = torch.randn(B, S, 2 * Hkv, D, generator=g)
+    q = torch.randn(B, 3, 3 * 8, D, generator=g)
+    kd, qd = kv.to(DEV), q.to(DEV)
+    kl = torch.tensor([777, 400], dtype=torch.int32, device=DEV)
+    out, lse = cp.window_decode(qd[:, :, 8:16], kd[:, :, :Hkv], kd[:, :, Hkv:], kl, left=300, sinks=4)
+    torch.cuda.synchronize()
+    k, v, qs = kv[:, :, :Hkv], kv[:, :, Hkv:], q[:, :, 8:16]
+    check(out, lse, ow.decode_attention(qs, k, v, D ** -0.5, [777, 400], 300, 4), qs, k, D ** -0.5, n=S)
 
 
 def test_decode_far_offsets():
