@@ -51,8 +51,9 @@ __device__ __forceinline__ int sequence_length(const WindowCall& c, int b) {
 // fp32 inputs, D <= 256, both forms (no accumulate).
 cudaError_t launch_window_f32(const WindowCall& c, cudaStream_t stream);
 
-// Tensor-core kernel: bf16 inputs, D 64 or 128.
+// Tensor-core kernel: bf16 inputs, D 64 or 128; and the time in microseconds to expect of it.
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream);
+double window_sm100_us(const WindowCall& c);
 
 // Single-token form (from_end, right = 0): bf16 inputs, D 64 or 128.
 cudaError_t launch_window_decode(const WindowCall& c, cudaStream_t stream);

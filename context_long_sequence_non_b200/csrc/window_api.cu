@@ -80,18 +80,15 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
 
 // Which kernel serves `window_decode`: the split one, which reads a sequence's keys once for every 16
 // (token, head) rows, or, for many tokens and heads, the tensor-core one with its 128-row tiles.
-// Time per visible key: the split kernel's passes of 4 D bytes come out of L2 at 7.8 TB/s; the
-// other takes 1.65 us for each 128 keys with a tile per SM, 2.4 us with two, and so on by waves.
-// Measured with a window of 4096, split / tiles: 8 sequences x 32 heads on 8, D = 128, 64 / 82 us
-// at 16 tokens, 138 / 81 at 32; 1 x 16 heads on 16, 36 / 56 at 128 tokens; 4 x 8 heads on 1, D = 64,
-// 42 / 47 at 128.
+// The split kernel's passes of 4 D bytes a key come out of L2 at 7.8 TB/s; the other knows its time.
+// Measured with a window of 4096, split / tiles (us): 8 sequences x 32 heads on 8, D = 128, 64 / 77
+// at 16 tokens, 138 / 78 at 32; 1 x 16 heads on 16, 16 / 17 at 32 tokens, 22 / 18 at 64; 4 x 8 heads
+// on 1, D = 64, 16 / 18 at 32, 30 / 18 at 64; 16 x 8 heads on 2, 1000 keys, 13 / 16 at 16, 20 / 16 at 32.
 bool tiles_serve(const WindowCall& c) {
-  const double sms = cpattn::sm_count();
   const double passes = double(c.B) * c.Hkv * (((long long)(c.H / c.Hkv) * c.Sq + 15) / 16);
-  const double tiles = double(c.B) * c.H * ((c.Sq + 127) / 128);
-  const double split = passes * 4 * c.D / 7.8e6;
-  const double waves = tiles <= sms ? 1.65 : 2.4 * std::ceil(tiles / (2 * sms));
-  return waves / 128 < split;
+  double keys = c.Skv;
+  if (c.left >= 0 && double(c.sinks) + c.left + c.Sq < keys) keys = double(c.sinks) + c.left + c.Sq;
+  return cpattn::window_sm100_us(c) < 3.5 + passes * keys * 4 * c.D / 7.8e6;
 }
 
 }  // namespace

@@ -24,7 +24,14 @@
 // stands between a handoff and the S after next.  One buffer of 128 keys, S behind P V, took 3 to 8%
 // longer on every case although its products are wider (N = 64 runs at about 70% of the N = 128
 // rate): each block then paid a wake-up, P V and Q K^T between two softmaxes.
-// The bf16 epilogue leaves through shared memory and one TMA store a tile.
+// A bf16 result leaves through shared memory and one TMA store a tile; fp32 and merged ones through
+// shared memory and whole rows a warp, the running O's loads issued before the last product
+// is done (one 64-key block merged into 256 x 2 heads in fp32: 6.3 us; 9.1 with each thread on its
+// own row).
+//
+// Few tiles.  Where they leave SMs idle, a cluster of 2, 4 or 8 CTAs shares the key blocks of a tile
+// and folds its parts (m, l, O) through distributed shared memory, each CTA 128 / n rows, in a fixed
+// order (plan below): 8 tiles of 1540 keys 20 -> 8.4 us, 76 tiles of 2400 29 -> 19.
 //
 // What bounds it.  64 keys cost a softmax warp 1475 cycles with its neighbour on the same scheduler:
 // 850 in the exponentials (512 of them the special-function unit's), 220 from S to the row maximum,
@@ -32,7 +39,7 @@
 // share of the exponentials to the FMA pipe (1, 2 or 3 of 8, a polynomial) changes nothing.  At the
 // large sizes the card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x
 // 16 heads, causal window 4096 with 64 sinks, 1.42 ms = 1010 TFLOP/s of visible products;
-// 4608 x 24, 512 to either side with 512 sinks, 100 us = 790 TFLOP/s.  Tried and not kept, on the
+// 4608 x 24, 512 to either side with 512 sinks, 97 us = 815 TFLOP/s.  Tried and not kept, on the
 // 128-key form: two 128-row tiles in one CTA with shared K and V, one CTA per item (2% slower on
 // the first case, 40% at 333 rows) and persistent over items (19% slower).
 //
@@ -42,6 +49,7 @@
 // product.
 // Every wait is bounded (mbar_wait): a stalled pipeline sets the device error word and the CTA
 // drains and exits.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "api_common.h"
@@ -51,6 +59,8 @@
 
 namespace cpattn {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kBlockM = 128;
 constexpr int kBlockN = 64;
@@ -63,6 +73,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMinorWeightInv = 8;   // see attn_sm100.cu
 constexpr int kPairs = kBlockN / 2;
+constexpr int kMaxCluster = 8;
 
 template <int D>
 struct Geometry {
@@ -78,6 +89,8 @@ struct Geometry {
   static constexpr int kOffV = kOffK + kK * kTileBytes;
   static constexpr int kOffBars = kOffV + kV * kTileBytes;
   static constexpr int kSmem = kOffBars + 256;
+  static constexpr int kOffParts = kBlockM * D * 4;  // behind a staged O: its rows' m and l
+  static_assert(kOffParts + kBlockM * 8 <= kOffBars);
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -94,8 +107,10 @@ static_assert(sizeof(Barriers) <= 256, "barrier block");
 // The key blocks of one tile: n_early blocks from key 0, then blocks from key w0.
 struct Blocks {
   int early, lo, hi;  // keys that some row of the tile sees: [0, early) and [lo, hi)
-  int n_early, w0, n;
+  int n_early, w0;
+  int first, n;  // this block's share of them: n from block `first` on
   __device__ __forceinline__ int base(int j) const {
+    j += first;
     return j < n_early ? j * kBlockN : w0 + (j - n_early) * kBlockN;
   }
   // does some row of the tile see every key of [k0, k1)?
@@ -104,7 +119,8 @@ struct Blocks {
   }
 };
 
-__device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, int p_last, int len) {
+__device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, int p_last, int len, int rank,
+                                              int n_ranks) {
   const KeyRange a = visible_keys(p_first, c.left, c.right, c.sinks, len);
   const KeyRange z = visible_keys(p_last, c.left, c.right, c.sinks, len);
   Blocks t;
@@ -114,7 +130,10 @@ __device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, 
   if (t.early >= t.lo) t.early = 0, t.lo = 0;  // one range
   t.n_early = (t.early + kBlockN - 1) / kBlockN;
   t.w0 = t.lo > t.n_early * kBlockN ? t.lo : t.n_early * kBlockN;
-  t.n = t.n_early + (t.hi > t.w0 ? (t.hi - t.w0 + kBlockN - 1) / kBlockN : 0);
+  const int all = t.n_early + (t.hi > t.w0 ? (t.hi - t.w0 + kBlockN - 1) / kBlockN : 0);
+  const int share = (all + n_ranks - 1) / n_ranks;
+  t.first = min(rank * share, all);
+  t.n = min(share, all - t.first);
   return t;
 }
 
@@ -142,7 +161,130 @@ enum Result : int {
   kMergeFrom32 = 2  // merged with the running (o_run fp32, lse) into bf16 out
 };
 
-template <int D, bool kOutF32, int kResult>
+// What a row's sum over keys (reference m in units of log2, sum l) and, merging, the running row
+// (log-sum-exp la) come to: O = fa running + fc new.
+struct RowEnd {
+  float fa, fc, lse;
+  bool write;
+};
+
+template <int kResult>
+__device__ __forceinline__ RowEnd finish_row(float m, float l, float la, bool in_range) {
+  const bool empty = m == -INFINITY;
+  const float lc2 = m + log2f(l);
+  RowEnd r{0.f, empty ? 0.f : 1.0f / l, empty ? -INFINITY : lc2 * kLn2, in_range};
+  if constexpr (kResult != kWrite) {
+    if (kResult == kMerge && empty) r.write = false;  // nothing to add: the running row stays as it is
+    if (empty) {  // the running row alone, rounded (0 when it is empty too)
+      r.fa = la == -INFINITY ? 0.f : 1.f;
+      r.lse = la;
+    } else {
+      const float la2 = la * kLog2e;
+      const float mx = fmaxf(la2, lc2);
+      const float wa = exp2f(la2 - mx), wc = exp2f(lc2 - mx);
+      const float tot = wa + wc;
+      r.fa = wa / tot;
+      r.fc = wc / (tot * l);
+      r.lse = (mx + log2f(tot)) * kLn2;
+    }
+  }
+  return r;
+}
+
+// The rows of a tile that one of its N blocks finishes: parts (m, l, O), each in its block's shared
+// memory, added in the order of the parts.  16 remote reads of 16 bytes a lane are in flight.
+template <int D, bool kOutF32, int kResult, int N>
+__device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluster_group& cluster, uint8_t* smem,
+                                           int q_first, int b, int h) {
+  constexpr bool kAcc = kResult != kWrite;
+  constexpr int kShare = kBlockM / N / 4;  // rows of a warp
+  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes, kRows = 16 / N;  // of a row; of an instruction; in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = (int(cluster.block_rank()) * 4 + warp) * kShare;
+  float* ml = reinterpret_cast<float*>(smem + Geometry<D>::kOffParts);
+  float w[N], l = 0.f, la = 0.f, m = -INFINITY;  // of row r0 + lane
+  const int mine = r0 + min(lane, kShare - 1);
+  const bool in_range = q_first + mine < c.Sq;
+  const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + (in_range ? q_first + mine : 0);
+  if (kAcc) la = c.lse[lse_idx];
+  float lk[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    w[k] = *cluster.map_shared_rank(ml + mine, k);
+    lk[k] = *cluster.map_shared_rank(ml + kBlockM + mine, k);
+  }
+  const int sub = lane / kLanes, vec = lane % kLanes;
+  const size_t out_at = ((size_t(b) * c.Sq + q_first + r0 + sub) * c.H + h) * size_t(D) + 4 * vec;
+  const size_t step = size_t(kAtOnce) * c.H * D;
+  RowEnd end;
+#pragma unroll
+  for (int s0 = 0; s0 < kShare / kAtOnce; s0 += kRows) {
+    float4 x[kRows][N], run[kAcc ? kRows : 1];
+#pragma unroll
+    for (int s = 0; s < kRows; ++s) {
+      if (s0 + s >= kShare / kAtOnce) continue;
+      const int r = r0 + kAtOnce * (s0 + s) + sub;
+      float4* part = reinterpret_cast<float4*>(smem) + r * (D / 4) + (vec ^ (r & 7));
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[s][k] = *cluster.map_shared_rank(part, k);
+      if constexpr (kAcc) {
+        run[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q_first + r < c.Sq) {
+          const size_t at = out_at + (s0 + s) * step;
+          if constexpr (kResult == kMergeFrom32) {
+            run[s] = *reinterpret_cast<const float4*>(c.o_run + at);
+          } else if constexpr (kOutF32) {
+            run[s] = *reinterpret_cast<const float4*>(static_cast<const float*>(c.out) + at);
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(c.out) + at);
+            run[s] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+          }
+        }
+      }
+    }
+    if (s0 == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) m = fmaxf(m, w[k]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        w[k] = w[k] == -INFINITY ? 0.f : ex2(w[k] - m);  // 0: that part saw no key
+        l = fmaf(w[k], lk[k], l);
+      }
+      end = finish_row<kResult>(m, l, la, in_range);
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[k] *= end.fc;
+      if (lane < kShare && end.write && c.lse != nullptr) c.lse[lse_idx] = end.lse;
+    }
+#pragma unroll
+    for (int s = 0; s < kRows; ++s) {
+      if (s0 + s >= kShare / kAtOnce) continue;
+      const int i = kAtOnce * (s0 + s) + sub;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (kAcc) {
+        const float f = __shfl_sync(0xffffffffu, end.fa, i);
+        if (f != 0.f)  // an empty running row may hold anything
+          o = make_float4(f * run[s].x, f * run[s].y, f * run[s].z, f * run[s].w);
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w[k], i);
+        o.x = fmaf(wk, x[s][k].x, o.x), o.y = fmaf(wk, x[s][k].y, o.y);
+        o.z = fmaf(wk, x[s][k].z, o.z), o.w = fmaf(wk, x[s][k].w, o.w);
+      }
+      const int live = __shfl_sync(0xffffffffu, int(end.write), i);
+      const size_t at = out_at + (s0 + s) * step;
+      if (live) {
+        if constexpr (kOutF32) *reinterpret_cast<float4*>(static_cast<float*>(c.out) + at) = o;
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + at) =
+              make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      }
+    }
+  }
+}
+
+template <int D, bool kOutF32, int kResult, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2)
     window_sm100_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowCall c,
@@ -160,9 +302,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   // on short ones.  Head by head instead it ends on the last head's full range: causal 8192 x 16 heads
   // 302 us against 264, a ring step's 5520 rows x 16 heads in 3 parts 385 against 357, 4608 x 24 103
   // against 100; 44160 x 16, where a head alone fills the GPU, 1450 against 1462
-  const unsigned n_heads = unsigned(c.H) * unsigned(c.B);
-  const int tile = int((gridDim.x - 1 - blockIdx.x) / n_heads);
-  const int bh = int(blockIdx.x % n_heads);
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = kSplit ? int(cluster.block_rank()) : 0, n_ranks = kSplit ? int(cluster.num_blocks()) : 1;
+  const unsigned n_heads = unsigned(c.H) * unsigned(c.B), item = blockIdx.x / unsigned(n_ranks);
+  const int tile = int((gridDim.x / unsigned(n_ranks) - 1 - item) / n_heads);
+  const int bh = int(item % n_heads);
   const int b = bh / c.H, h = bh - b * c.H;
   const int q_first = tile * kBlockM;
   volatile int* abort_flag = &bars.abort;
@@ -196,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int len = sequence_length(c, b);
   const int off = c.from_end ? len - c.Sq : c.off;
   const int last_row = min(q_first + kBlockM, c.Sq) - 1;
-  const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len);
+  const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len, rank, n_ranks);
   // The first loads go out before the block meets: nothing waits on their barriers earlier, and
   // their latency covers the rest of the set-up.
   const int kvh = c.Hkv == c.H ? h : h / (c.H / c.Hkv);
@@ -344,9 +488,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ------------------------------------------------------------------ epilogue
-    const int qr = in_range ? q : 0;
-    const size_t row_off = ((size_t(b) * c.Sq + qr) * c.H + h) * size_t(D);
-    const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + qr;
+    const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + (in_range ? q : 0);
+    // Results other than a bf16 tile that leaves by TMA go through shared memory, so that a warp reads
+    // 16 bytes a lane of whole rows of the running O, kBatch instructions at a time, and writes whole
+    // rows.  (Each thread on its own row: 32 rows an instruction, and a read before every write.)
+    constexpr bool kRun32 = kOutF32 || kResult == kMergeFrom32;
+    constexpr int kCols = kRun32 ? 4 : 8, kLanes = D / kCols;  // of a lane; of a row
+    constexpr int kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kBatch = kSteps < 16 ? kSteps : 16;
+    const int sub = lane / kLanes, col = kCols * (lane % kLanes);
+    const int warp_first = q_first + warp * 32;
+    const size_t out_at = ((size_t(b) * c.Sq + warp_first + sub) * c.H + h) * size_t(D) + col;
+    const size_t step = size_t(kAtOnce) * c.H * D;
+    auto running = [&](int s) {  // the lane's columns of row kAtOnce s + sub
+      if (warp_first + kAtOnce * s + sub >= c.Sq) return make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kResult == kMergeFrom32) return *reinterpret_cast<const uint4*>(c.o_run + out_at + s * step);
+      else if constexpr (kOutF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(c.out) + out_at + s * step);
+      else return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.out) + out_at + s * step);
+    };
+    uint4 run[kAcc ? kBatch : 1];
+    float la = 0.f;
+    if constexpr (kAcc) {
+      if constexpr (!kSplit) {  // on their way while the last products run
+        la = c.lse[lse_idx];
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) run[s] = running(s);
+      }
+    }
     if (ok && blk.n > 0) {
       ok = mbar_wait(smem_u32(&bars.o_full), 0, abort_flag, err, wait_limit);
       ok = __all_sync(0xffffffffu, ok);
@@ -355,29 +522,35 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       const float l = (l0.x + l0.y) + (l1.x + l1.y);
       const bool empty = m == -INFINITY;
-      const float lc2 = m + log2f(l);
-      float fa = 0.f, fc = empty ? 0.f : 1.0f / l;
-      float lse_out = empty ? -INFINITY : lc2 * kLn2;
-      bool write = in_range;
-      if constexpr (kAcc) {
-        if (kResult == kMerge && empty) write = false;  // nothing to add: the running row stays as it is
-        if (write) {
-          const float la = c.lse[lse_idx];
-          if (empty) {  // the running row alone, rounded (0 when it is empty too)
-            fa = la == -INFINITY ? 0.f : 1.f;
-            lse_out = la;
-          } else {
-            const float la2 = la * kLog2e;
-            const float mx = fmaxf(la2, lc2);
-            const float wa = exp2f(la2 - mx), wc = exp2f(lc2 - mx);
-            const float tot = wa + wc;
-            fa = wa / tot;
-            fc = wc / (tot * l);
-            lse_out = (mx + log2f(tot)) * kLn2;
+      const RowEnd end = finish_row<kResult>(m, l, la, in_range);
+      const float fa = end.fa, fc = kSplit ? 1.f : end.fc, lse_out = end.lse;
+      const bool write = end.write;
+      // O times fc into shared memory: rows of D fp32, their 16-byte vectors permuted by the row so
+      // that neither writing nor reading conflicts
+      const uint32_t mine = smem_base + uint32_t(warp) * 32u * D * 4u;
+      auto stage = [&]() {
+#pragma unroll 1
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t t[32];
+          if (blk.n > 0) tmem_ld32(t_o + oc * 32, t);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = empty ? 0.f : __uint_as_float(t[4 * e + i]) * fc;
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             mine + uint32_t(lane) * D * 4u + ((uint32_t(oc * 8 + e) ^ (uint32_t(lane) & 7u)) << 4)),
+                         "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3])
+                         : "memory");
           }
         }
-      }
-      if constexpr (!kOutF32 && !kAcc) {
+      };
+      if constexpr (kSplit) {  // a part, folded below
+        stage();
+        float* ml = reinterpret_cast<float*>(smem + G::kOffParts);
+        ml[row] = m;
+        ml[kBlockM + row] = l;
+      } else if constexpr (!kOutF32 && !kAcc) {
         // bf16 rows go to global memory as one tile: each thread writes its row into Q's shared
         // memory (read for the last time before O was complete) in the 128-byte swizzle, and a TMA
         // store takes it from there, leaving out rows past Sq.  Row-by-row stores, 32 rows of
@@ -404,67 +577,66 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
         fence_proxy_async_smem();
       } else {
-#pragma unroll 1
-      for (int oc = 0; oc < D / 32; ++oc) {
-        uint32_t t[32];
+        stage();
         __syncwarp();
-        if (blk.n > 0) tmem_ld32(t_o + oc * 32, t);
-        if (!write) continue;
-        if (empty) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t[e] = 0u;
-        }
-        if constexpr (kOutF32) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(c.out) + row_off + oc * 32);
+        for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+          uint4 next[kAcc ? kBatch : 1];
+          if constexpr (kAcc) {
+            if (s0 + kBatch < kSteps) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float4 v = make_float4(__uint_as_float(t[4 * e]) * fc, __uint_as_float(t[4 * e + 1]) * fc,
-                                   __uint_as_float(t[4 * e + 2]) * fc, __uint_as_float(t[4 * e + 3]) * fc);
-            if (kAcc && fa != 0.f) {  // an empty accumulator row is never read
-              const float4 a = dst[e];
-              v.x = fmaf(fa, a.x, v.x);
-              v.y = fmaf(fa, a.y, v.y);
-              v.z = fmaf(fa, a.z, v.z);
-              v.w = fmaf(fa, a.w, v.w);
+              for (int s = 0; s < kBatch; ++s) next[s] = running(s0 + kBatch + s);
             }
-            dst[e] = v;
           }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + row_off + oc * 32);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float o[8];
+          for (int s = 0; s < kBatch; ++s) {
+            const int r = kAtOnce * (s0 + s) + sub;
+            float o[kCols];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(t[8 * e + i]) * fc;
-            if (kResult == kMergeFrom32 && fa != 0.f) {
-              const float4* run = reinterpret_cast<const float4*>(c.o_run + row_off + oc * 32 + e * 8);
-              const float4 a = run[0], z = run[1];
-              o[0] = fmaf(fa, a.x, o[0]), o[1] = fmaf(fa, a.y, o[1]), o[2] = fmaf(fa, a.z, o[2]), o[3] = fmaf(fa, a.w, o[3]);
-              o[4] = fmaf(fa, z.x, o[4]), o[5] = fmaf(fa, z.y, o[5]), o[6] = fmaf(fa, z.z, o[6]), o[7] = fmaf(fa, z.w, o[7]);
-            } else if (kAcc && fa != 0.f) {
-              const uint4 a = dst[e];
-              const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+            for (int v = 0; v < kCols / 4; ++v)
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(o[4 * v]), "=f"(o[4 * v + 1]), "=f"(o[4 * v + 2]), "=f"(o[4 * v + 3])
+                           : "r"(mine + uint32_t(r) * D * 4u + (uint32_t(col / 4 + v) ^ (uint32_t(r) & 7u)) * 16u));
+            if constexpr (kAcc) {
+              const float f = __shfl_sync(0xffffffffu, fa, r);
+              const uint32_t w[4] = {run[s].x, run[s].y, run[s].z, run[s].w};
+              if (f != 0.f) {  // an empty running row may hold anything
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                o[2 * i] = fmaf(fa, __uint_as_float(aw[i] << 16), o[2 * i]);
-                o[2 * i + 1] = fmaf(fa, __uint_as_float(aw[i] & 0xFFFF0000u), o[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                  if constexpr (kRun32) {
+                    o[i] = fmaf(f, __uint_as_float(w[i]), o[i]);
+                  } else {
+                    o[2 * i] = fmaf(f, __uint_as_float(w[i] << 16), o[2 * i]);
+                    o[2 * i + 1] = fmaf(f, __uint_as_float(w[i] & 0xFFFF0000u), o[2 * i + 1]);
+                  }
+                }
               }
             }
-            uint4 v;
-            v.x = pack_bf16x2(o[0], o[1]);
-            v.y = pack_bf16x2(o[2], o[3]);
-            v.z = pack_bf16x2(o[4], o[5]);
-            v.w = pack_bf16x2(o[6], o[7]);
-            dst[e] = v;
+            const int live = __shfl_sync(0xffffffffu, int(write), r);
+            const size_t at = out_at + (s0 + s) * step;
+            if (live) {
+              if constexpr (kOutF32)
+                *reinterpret_cast<float4*>(static_cast<float*>(c.out) + at) = make_float4(o[0], o[1], o[2], o[3]);
+              else if constexpr (kCols == 4)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + at) =
+                    make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+              else
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.out) + at) =
+                    make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                               pack_bf16x2(o[6], o[7]));
+            }
+          }
+          if constexpr (kAcc) {
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) run[s] = next[s];
           }
         }
-      }
         if (write && c.lse != nullptr) c.lse[lse_idx] = lse_out;
       }
     }
     if constexpr (!kOutF32 && !kAcc) {
       // every softmax warp comes here, also one whose wait ran out
-      if (bar_and(1, 128, ok) && threadIdx.x == 0) {
+      if (!kSplit && bar_and(1, 128, ok) && threadIdx.x == 0) {
 #pragma unroll
         for (int bx = 0; bx < G::kBoxes; ++bx)
           tma_store_4d(&tm_o, smem_base + bx * G::kQBoxBytes, bx * 64, h, q_first, b);
@@ -599,6 +771,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
+  if constexpr (kSplit) {
+    // fold the parts: each block finishes 128 / n_ranks rows, the sums in the order of the parts
+    cluster.sync();
+    if (warp < 4) {
+      if (n_ranks == 2) fold_parts<D, kOutF32, kResult, 2>(c, cluster, smem, q_first, b, h);
+      else if (n_ranks == 4) fold_parts<D, kOutF32, kResult, 4>(c, cluster, smem, q_first, b, h);
+      else fold_parts<D, kOutF32, kResult, 8>(c, cluster, smem, q_first, b, h);
+    }
+    cluster.sync();  // no block leaves while another reads its shared memory
+  }
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -620,26 +803,67 @@ bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kOutF32, int kResult>
-cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+// Blocks that share a query tile's keys, and the time (us) that the kernel is then expected to take.  A
+// tile walks 0.66 us per block of 64 keys, 0.95 beside another on its SM; parts cost 1.9 us to
+// start and fold, 4 when they are more than the SMs.  Clusters of four and eight do not fill
+// every SM.  Measured, parts 1 / 2 / 4 / 8: 20 tiles of 512 keys 9.9 / 9.2 / 7.9 / 10.3 us, of 2048
+// 25.8 / 17.5 / 12.6 / 14.1; 100 tiles of 1024 15.7 / 16.2 (200 blocks), of 4096 47.6 / 38.2; 48 tiles of
+// 2048 26.5 / 18.5 / 18.1; 37 tiles of 512 10.1 / 9.4 / 10.7 / 16.9.
+struct Plan {
+  int parts;
+  double us;
+};
+
+Plan plan(const WindowCall& c) {
+  const long long items = (long long)((c.Sq + kBlockM - 1) / kBlockM) * c.H * c.B, sms = sm_count();
+  long long keys = c.Skv, early = 0;  // of a tile, at most
+  if (c.left >= 0 && c.right >= 0 && (long long)c.left + c.right + kBlockM < keys) {
+    keys = (long long)c.left + c.right + kBlockM;
+    early = c.sinks < c.Skv - keys ? c.sinks : c.Skv - keys;
+  }
+  const long long blocks = (keys + kBlockN - 1) / kBlockN + (early + kBlockN - 1) / kBlockN;
+  if (items > sms) return {1, 5.0 + double((items + 2 * sms - 1) / (2 * sms)) * double(blocks) * 1.2};
+  Plan best{1, 5.0 + 0.66 * double(blocks)};
+  for (int n = 2; n <= kMaxCluster && 2 * items * n <= (n == 2 ? 4 : 3) * sms; n *= 2) {
+    const double own = double((blocks + n - 1) / n);
+    const double t = 5.0 + (items * n * (n == 2 ? 20 : 23) <= 20 * sms ? 1.9 + 0.66 * own : 4.0 + 0.95 * own);
+    if (t < best.us) best = {n, t};
+  }
+  return best;
+}
+
+template <int D, bool kOutF32, int kResult, bool kSplit>
+cudaError_t launch_parts(const WindowCall& c, int n_ranks, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& to, int* err, cudaStream_t stream) {
-  auto kernel = window_sm100_kernel<D, kOutF32, kResult>;
+  auto kernel = window_sm100_kernel<D, kOutF32, kResult, kSplit>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM) * unsigned(c.H) * unsigned(c.B));
+  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM) * unsigned(c.H) * unsigned(c.B) * unsigned(n_ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Geometry<D>::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(n_ranks);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kSplit ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, to,
                             float(double(c.scale) * 1.4426950408889634074),
                             kRescaleLog2, err, kDefaultWaitLimit);
+}
+
+template <int D, bool kOutF32, int kResult>
+cudaError_t launch(const WindowCall& c, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CUtensorMap& to, int* err, cudaStream_t stream) {
+  const int n = plan(c).parts;
+  return n > 1 ? launch_parts<D, kOutF32, kResult, true>(c, n, tq, tk, tv, to, err, stream)
+               : launch_parts<D, kOutF32, kResult, false>(c, 1, tq, tk, tv, to, err, stream);
 }
 
 template <int D>
@@ -654,6 +878,8 @@ cudaError_t launch_d(const WindowCall& c, const CUtensorMap& tq, const CUtensorM
 }
 
 }  // namespace
+
+double window_sm100_us(const WindowCall& c) { return plan(c).us; }
 
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, to;

@@ -254,6 +254,52 @@ def test_ring_step(acc_dtype, w):
     check(out, lse, ref, q, k, D ** -0.5, merges=4)
 
 
+# Few tiles share their keys out to clusters of 2, 4 and 8; from 149 on (24 heads of 7) each has its own.
+@pytest.mark.parametrize("B,H,Hkv,Sq,Skv,D", [(1, 1, 1, 1, 4000, 128), (1, 2, 1, 130, 2000, 64), (2, 3, 3, 300, 900, 128),
+                                              (1, 10, 2, 128, 1500, 64), (1, 40, 8, 190, 1100, 128),
+                                              (1, 24, 4, 800, 700, 128), (2, 12, 12, 890, 500, 64)])
+@pytest.mark.parametrize("w", [dict(left=-1, right=-1), dict(left=300, right=0, sinks=70), dict(left=-1, right=0)])
+def test_tiles_and_parts_in_every_form_of_result(B, H, Hkv, Sq, Skv, D, w):
+    q, k, v = make(28 + Sq, B, H, Hkv, Sq, Skv, D)
+    at = max(Skv - Sq, 0)
+    o, l = run_window(q, k, v, q_pos=at, **w)
+    again = run_window(q, k, v, q_pos=at, **w)
+    assert torch.equal(o, again[0]) and torch.equal(l, again[1])  # sums in a fixed order
+    run_window(q, k, v, q_pos=at, out_dtype=torch.float32, **w)
+    run_window(q, k, v, kv_len=[Skv // 9] * B, q_pos=at, out_dtype=torch.float32, **w)  # parts without keys
+    cuts = [0, Skv // 2 + 3, Skv - 5, Skv]
+    ks = [k[:, a:b].contiguous().to(DEV) for a, b in zip(cuts, cuts[1:])]
+    vs = [v[:, a:b].contiguous().to(DEV) for a, b in zip(cuts, cuts[1:])]
+    ref = ow.window_attention(q, k, v, D ** -0.5, q_pos=at, **w)
+    for acc_dtype in (None, torch.bfloat16, torch.float32):
+        run = torch.empty(q.shape, dtype=acc_dtype or torch.float32, device=DEV)
+        out, lse = run if acc_dtype else torch.empty_like(q, device=DEV), torch.empty((B, H, Sq), device=DEV)
+        for c, (kc, vc) in enumerate(zip(ks, vs)):
+            last = c == 2 and acc_dtype is None
+            cp.window_fwd(q.to(DEV), kc, vc, out=out if last else run, run=run if last else None, lse=lse,
+                          accumulate=c > 0, q_pos=at, k_pos=cuts[c], **w)
+        torch.cuda.synchronize()
+        check(out, lse, ref, q, k, D ** -0.5, merges=3)
+
+
+def test_merge_into_rows_that_hold_anything():
+    # running rows with LSE = -inf are never used, whatever they hold; rows that see nothing stay
+    for B, H, Sq, Skv in ((1, 2, 200, 900), (2, 20, 500, 300)):
+        q, k, v = make(29, B, H, H, Sq, Skv, 128)
+        qd, kd, vd = (x.to(DEV) for x in (q, k, v))
+        w = dict(left=150, right=0, q_pos=100, k_pos=200)
+        ref = ow.window_attention(q, k, v, 128 ** -0.5, **w)
+        sees = torch.from_numpy(~np.isneginf(ref[1])).transpose(1, 2)
+        for dt in (torch.float32, torch.bfloat16):
+            out = torch.full((B, Sq, H, 128), float("nan"), dtype=dt, device=DEV)
+            lse = torch.full((B, H, Sq), -math.inf, device=DEV)
+            cp.window_fwd(qd, kd, vd, out=out, lse=lse, accumulate=True, **w)
+            torch.cuda.synchronize()
+            assert torch.isnan(out.cpu()[~sees]).all() and (~sees).any()
+            filled = torch.where(sees[..., None], out.cpu(), torch.zeros((), dtype=dt))
+            check(filled, lse, ref, q, k, 128 ** -0.5, merges=1)
+
+
 def test_last_chunk_out_of_a_float32_running_result():
     q, k, v = make(23, 1, 2, 2, 300, 100, 64)
     run = torch.full((1, 300, 2, 64), float("nan"), device=DEV)
