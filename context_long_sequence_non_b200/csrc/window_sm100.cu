@@ -131,9 +131,13 @@ __device__ __forceinline__ Blocks tile_blocks(const WindowCall& c, int p_first, 
   t.n_early = (t.early + kBlockN - 1) / kBlockN;
   t.w0 = t.lo > t.n_early * kBlockN ? t.lo : t.n_early * kBlockN;
   const int all = t.n_early + (t.hi > t.w0 ? (t.hi - t.w0 + kBlockN - 1) / kBlockN : 0);
-  const int share = (all + n_ranks - 1) / n_ranks;
-  t.first = min(rank * share, all);
-  t.n = min(share, all - t.first);
+  t.first = 0;
+  t.n = all;
+  if (n_ranks > 1) {
+    const int share = (all + n_ranks - 1) / n_ranks;
+    t.first = min(rank * share, all);
+    t.n = min(share, all - t.first);
+  }
   return t;
 }
 
