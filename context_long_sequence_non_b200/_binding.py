@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -76,6 +77,7 @@ def lib() -> ctypes.CDLL:
             L.cpattn_rope.argtypes = [vp] * 4 + [i] * 7 + [f, ll, ll, i, vp]
             L.cpattn_qk_norm_rope.argtypes = [vp] * 8 + [i] * 8 + [f] * 3 + [ll] * 4 + [i, vp]
             L.cpattn_seq2head_qkv_norm_rope.argtypes = [vp] * 10 + [i] * 7 + [f] * 3 + [vp]
+            L.cpattn_call.argtypes = [i, ctypes.c_char_p, i]
             L.cpattn_status_str.argtypes = [i]
             L.cpattn_status_str.restype = ctypes.c_char_p
             L.cpattn_device_error.argtypes = []
@@ -88,7 +90,7 @@ def lib() -> ctypes.CDLL:
                          "cpattn_device_error", "cpattn_selftest_wait_timeout", "cpattn_version",
                          "cpattn_selftest_exp2", "cpattn_window_fwd", "cpattn_window_decode",
                          "cpattn_rope_frequencies", "cpattn_rope", "cpattn_qk_norm_rope",
-                         "cpattn_seq2head_qkv_norm_rope"):
+                         "cpattn_seq2head_qkv_norm_rope", "cpattn_call"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -439,22 +441,39 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(index, stream, what, fn, args):
+class _Entry:
+    """A call that goes through cpattn_call: its number and the layout of its words (P pointer,
+    q integer, d float; the stream is the last P)."""
+
+    def __init__(self, name, code, layout):
+        self.name, self.code, self.n = name, code, struct.calcsize("=" + layout.replace("P", "Q")) // 8
+        self.pack = struct.Struct("=" + layout.replace("P", "Q")).pack
+
+
+_WINDOW_FWD = _Entry("cpattn_window_fwd", 0, "7P9qd8qP")
+_WINDOW_DECODE = _Entry("cpattn_window_decode", 1, "6P9qd4qP")
+_ROPE = _Entry("cpattn_rope", 2, "4P7qd3qP")
+_QK_NORM_ROPE = _Entry("cpattn_qk_norm_rope", 3, "8P8q3d5qP")
+_SEQ2HEAD_QKV_NORM_ROPE = _Entry("cpattn_seq2head_qkv_norm_rope", 4, "10P7q3dP")
+
+
+def _call(index, stream, entry, *args):
     """Run a library call with CUDA device ``index`` current (the library launches on the current
-    device) on ``stream``, or on that device's current stream."""
+    device) on ``stream``, or on that device's current stream.  Pointers are addresses, 0: none."""
     if stream is None:
         raw = _raw_stream(index)
     elif stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:
         raw = stream.cuda_stream
+    words = entry.pack(*args, raw)
     if _current_device() == index:
-        st = fn(*args, raw)
+        st = lib().cpattn_call(entry.code, words, entry.n)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, raw)
+            st = lib().cpattn_call(entry.code, words, entry.n)
     if st != OK:
-        raise CpattnError(st, what)
+        raise CpattnError(st, entry.name)
 
 
 def _same_device(first, *ts):
@@ -502,6 +521,13 @@ def _packed(t, shape, name, dtype):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _packed_like(t, dtype):
+    """A new contiguous tensor of t's shape.  (A contiguous t's own layout will do, in half the time.)"""
+    if t.is_contiguous():
+        return torch.empty_like(t) if t.dtype == dtype else torch.empty_like(t, dtype=dtype)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def _extent(n, name):
     n = int(n)
     if not -(1 << 31) <= n < 1 << 31:
@@ -529,13 +555,13 @@ def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
     if kv_len is not None:
         _packed(kv_len, (B,), "kv_len", torch.int32)
     if out is None:
-        out = torch.empty(q_shape, dtype=out_dtype or dtype, device=q.device)
+        out = _packed_like(q, out_dtype or dtype)
     else:
         _packed(out, q_shape, "out", out_dtype)
     if lse is not None:
         _packed(lse, (B, H, Sq), "lse", torch.float32)
     elif want_lse:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = torch.empty_strided((B, H, Sq), (H * Sq, Sq, 1), dtype=torch.float32, device=q.device)
     index = _same_device(q, k, v, kv_len, out, lse)
     codes = _CODE.get(dtype), _CODE.get(out.dtype)
     if None in codes:
@@ -564,12 +590,11 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
     index, dims, codes, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
     if run is not None:
         _same_device(q, run)
-    _call(index, stream, "cpattn_window_fwd", lib().cpattn_window_fwd,
-          (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-           None if lse is None else lse.data_ptr(), None if kv_len is None else kv_len.data_ptr(),
-           None if run is None else run.data_ptr(), *dims, _extent(q_pos, "q_pos"),
-           _extent(k_pos, "k_pos"), _extent(left, "left"), _extent(right, "right"),
-           _extent(sinks, "sinks"), *codes, 1 if accumulate else 0))
+    _call(index, stream, _WINDOW_FWD, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          0 if lse is None else lse.data_ptr(), 0 if kv_len is None else kv_len.data_ptr(),
+          0 if run is None else run.data_ptr(), *dims, _extent(q_pos, "q_pos"), _extent(k_pos, "k_pos"),
+          _extent(left, "left"), _extent(right, "right"), _extent(sinks, "sinks"), *codes,
+          1 if accumulate else 0)
     return out, lse
 
 
@@ -580,11 +605,9 @@ def window_decode(q, k_cache, v_cache, kv_len=None, left=-1, sinks=0, out=None, 
     sequence holds, the newest included (None: S_max).  See cpattn_window_decode."""
     index, dims, codes, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale, out_dtype,
                                                 want_lse)
-    _call(index, stream, "cpattn_window_decode", lib().cpattn_window_decode,
-          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-           None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
-           None if lse is None else lse.data_ptr(), *dims, _extent(left, "left"),
-           _extent(sinks, "sinks"), *codes))
+    _call(index, stream, _WINDOW_DECODE, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          0 if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
+          0 if lse is None else lse.data_ptr(), *dims, _extent(left, "left"), _extent(sinks, "sinks"), *codes)
     return out, lse
 
 
@@ -646,15 +669,16 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
     H, D = shape[-2], shape[-1]
     tokens = shape[0] if len(shape) == 3 else shape[:-2].numel()
     rows, axes, rot = _rope_args(tokens, pos, freq)
+    xs = 0 if x.is_contiguous() else _token_stride(x, "x")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-    elif out.shape != shape or out.dtype != dtype:
-        _need_shape(out, shape, "out", dtype)
+        out, ys = _packed_like(x, dtype), 0
+    else:
+        if out.shape != shape or out.dtype != dtype:
+            _need_shape(out, shape, "out", dtype)
+        ys = xs if out is x else _token_stride(out, "out")
     index = _same_device(x, pos, freq, out)
-    _call(index, stream, "cpattn_rope", lib().cpattn_rope,
-          (x.data_ptr(), out.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D, rot, axes,
-           1 if interleaved else 0, float(factor), _token_stride(x, "x"), _token_stride(out, "out"),
-           _dtype_code(dtype)))
+    _call(index, stream, _ROPE, x.data_ptr(), out.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, H, D,
+          rot, axes, 1 if interleaved else 0, float(factor), xs, ys, _dtype_code(dtype))
     return out
 
 
@@ -671,18 +695,19 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.
         if g.dtype != torch.float32 or g.shape != (D,) or not g.is_contiguous():
             raise ValueError("gamma_q and gamma_k must be float32 [D]")
     rows, axes, rot = _rope_args(tokens, pos, freq)
+    qs, ks = _token_stride(q, "q"), _token_stride(k, "k")
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    qo, ko = out
-    _need_shape(qo, q.shape, "out[0]", q.dtype)
-    _need_shape(ko, k.shape, "out[1]", k.dtype)
+        qo, ko, qos, kos = _packed_like(q, q.dtype), _packed_like(k, k.dtype), 0, 0
+    else:
+        qo, ko = out
+        _need_shape(qo, q.shape, "out[0]", q.dtype)
+        _need_shape(ko, k.shape, "out[1]", k.dtype)
+        qos, kos = _token_stride(qo, "out[0]"), _token_stride(ko, "out[1]")
     index = _same_device(q, k, gamma_q, gamma_k, pos, freq, qo, ko)
-    _call(index, stream, "cpattn_qk_norm_rope", lib().cpattn_qk_norm_rope,
-          (q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(), gamma_q.data_ptr(),
-           gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2], k.shape[-2],
-           D, rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor),
-           _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(qo, "out[0]"),
-           _token_stride(ko, "out[1]"), _dtype_code(q.dtype)))
+    _call(index, stream, _QK_NORM_ROPE, q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
+          gamma_q.data_ptr(), gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), tokens, rows, q.shape[-2],
+          k.shape[-2], D, rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor),
+          qs, ks, qos, kos, _dtype_code(q.dtype))
     return qo, ko
 
 
@@ -712,11 +737,10 @@ def seq2head_qkv_norm_rope(q, k, v, P, gamma_q, gamma_k, pos, freq, interleaved=
         if not t.is_contiguous():
             raise ValueError("q, k, v must be contiguous")
     index = _same_device(q, k, v, gamma_q, gamma_k, pos, freq, *out)
-    _call(index, stream, "cpattn_seq2head_qkv_norm_rope", lib().cpattn_seq2head_qkv_norm_rope,
-          (q.data_ptr(), k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out),
-           None if gamma_q is None else gamma_q.data_ptr(),
-           None if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H, D,
-           rot, axes, 1 if interleaved else 0, float(eps), float(out_scale), float(factor)))
+    _call(index, stream, _SEQ2HEAD_QKV_NORM_ROPE, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          *(t.data_ptr() for t in out), 0 if gamma_q is None else gamma_q.data_ptr(),
+          0 if gamma_k is None else gamma_k.data_ptr(), pos.data_ptr(), freq.data_ptr(), P, S_l, H, D, rot, axes,
+          1 if interleaved else 0, float(eps), float(out_scale), float(factor))
     return out
 
 

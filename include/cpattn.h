@@ -505,6 +505,23 @@ CPATTN_API int cpattn_seq2head_qkv_norm_rope(const void* q, const void* k, const
                                              int interleaved, float eps, float out_scale,
                                              float factor, cpattn_stream_t stream);
 
+/*
+ * cpattn_call -- one of the five calls above with its arguments as `n` words of 8 bytes, in their
+ * order: pointers and integers as 64-bit integers, floats as the bits of a double, the stream
+ * last.  For bindings of languages that pay for every argument of a foreign call (21 of them cost
+ * Python 3 us, more than the launch).  Errors: those of the call; CPATTN_ERR_SHAPE for an unknown
+ * entry, another number of words, or a word that an int cannot hold; CPATTN_ERR_NULL without words.
+ */
+typedef enum {
+  CPATTN_CALL_WINDOW_FWD = 0,
+  CPATTN_CALL_WINDOW_DECODE = 1,
+  CPATTN_CALL_ROPE = 2,
+  CPATTN_CALL_QK_NORM_ROPE = 3,
+  CPATTN_CALL_SEQ2HEAD_QKV_NORM_ROPE = 4
+} cpattn_entry;
+
+CPATTN_API int cpattn_call(int entry, const void* words, int n);
+
 /* Human-readable name of a cpattn_status value (static string, never NULL). */
 CPATTN_API const char* cpattn_status_str(int status);
 

@@ -3,6 +3,7 @@ any CUDA call, the frequency rules, and the binding's own checks."""
 
 import ctypes
 import math
+import re
 
 import numpy as np
 import pytest
@@ -292,3 +293,40 @@ def test_rope_binding_checks():
         cp.ring_attention(s, [], [], left=3)
     with pytest.raises(ValueError, match="needs chunks"):
         cp.ring_attention(s, [s], [s], left=3, k_pos=[0, 5])
+
+
+# ------------------------------------------------------------------ calls by number
+
+def test_calls_by_number_reach_the_same_checks(L):
+    w = [FAKE, FAKE + BIG, FAKE + 2 * BIG, FAKE + 3 * BIG, FAKE + 4 * BIG, 0, 0,
+         1, 4, 2, 8, 8, 128, 0, 0, 0, 0.1, 0, 0, 3, 0, 0, 0, 0, 0, 0]
+    good = B._WINDOW_FWD
+    assert good.n == len(w) == len(L.cpattn_window_fwd.argtypes)
+    for at, value, status in ((7, 0, B.ERR_SHAPE), (8, 5, B.ERR_SHAPE), (12, 96, B.ERR_UNSUPPORTED), (0, 0, B.ERR_NULL),
+                              (1, FAKE + 8, B.ERR_ALIGN), (16, -1.0, B.ERR_SHAPE), (16, math.nan, B.ERR_SHAPE),
+                              (10, (1 << 32) + 8, B.ERR_SHAPE),  # not cut to an int of 8
+                              (19, -(1 << 40), B.ERR_SHAPE), (13, 1 << 62, B.ERR_SHAPE), (13, -1, B.ERR_SHAPE),
+                              (22, 7, B.ERR_UNSUPPORTED)):
+        bad = list(w)
+        bad[at] = value
+        assert L.cpattn_call(good.code, good.pack(*bad), good.n) == status, (at, value)
+        if abs(value) < 1 << 31 or at == 13:
+            assert L.cpattn_window_fwd(*bad[:5], None, None, *bad[7:25], None) == status, (at, value)
+
+
+def test_calls_by_number_match_the_declared_arguments(L):
+    kinds = {"P": ctypes.c_void_p, "d": ctypes.c_float}
+    for e, layout in ((B._WINDOW_FWD, "7P9qd8qP"), (B._WINDOW_DECODE, "6P9qd4qP"), (B._ROPE, "4P7qd3qP"),
+                      (B._QK_NORM_ROPE, "8P8q3d5qP"), (B._SEQ2HEAD_QKV_NORM_ROPE, "10P7q3dP")):
+        flat = "".join(c * int(n or 1) for n, c in re.findall(r"(\d*)([Pqd])", layout))
+        declared = getattr(L, e.name).argtypes
+        assert len(flat) == e.n == len(declared)
+        for c, t in zip(flat, declared):
+            assert t is kinds[c] if c in kinds else t in (ctypes.c_int, ctypes.c_longlong)
+        zero = e.pack(*(0.0 if c == "d" else 0 for c in flat))
+        assert L.cpattn_call(e.code, zero, e.n) == B.ERR_SHAPE  # no sizes
+        assert L.cpattn_call(e.code, zero, e.n - 1) == B.ERR_SHAPE
+        assert L.cpattn_call(e.code, zero, e.n + 1) == B.ERR_SHAPE
+        assert L.cpattn_call(e.code, None, e.n) == B.ERR_NULL
+    for code in (-1, 5, 1 << 30):
+        assert L.cpattn_call(code, zero, 4) == B.ERR_SHAPE
