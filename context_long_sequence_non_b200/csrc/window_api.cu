@@ -81,9 +81,9 @@ int check(WindowCall* c, int in_dtype, int out_dtype) {
 // Which kernel serves `window_decode`: the split one, which reads a sequence's keys once for every 16
 // (token, head) rows, or, for many tokens and heads, the tensor-core one with its 128-row tiles.
 // The split kernel's passes of 4 D bytes a key come out of L2 at 7.8 TB/s; the other knows its time.
-// Measured with a window of 4096, split / tiles (us): 8 sequences x 32 heads on 8, D = 128, 64 / 77
-// at 16 tokens, 138 / 78 at 32; 1 x 16 heads on 16, 16 / 17 at 32 tokens, 22 / 18 at 64; 4 x 8 heads
-// on 1, D = 64, 16 / 18 at 32, 30 / 18 at 64; 16 x 8 heads on 2, 1000 keys, 13 / 16 at 16, 20 / 16 at 32.
+// Measured, split / tiles (us): 8 sequences x 32 heads on 8, D = 128, a window of 4096, 38 / 34 at 8
+// tokens, 138 / 36 at 32; 64 x 128 heads on 16, 5 tokens, 4000 keys, 533 / 279; 1 x 16 heads on 16,
+// 16 / 17 at 32 tokens, 22 / 18 at 64; 32 x 16 heads on 2, 2 tokens, 1000 keys, 10 / 13.
 bool tiles_serve(const WindowCall& c) {
   const double passes = double(c.B) * c.Hkv * (((long long)(c.H / c.Hkv) * c.Sq + 15) / 16);
   double keys = c.Skv;

@@ -7,7 +7,8 @@
 // moves only when a key above it could carry 1/kMinorWeightInv of the row or exceeds it by
 // rescale_log2, so that most blocks rescale nothing.
 //
-// One CTA takes 128 query rows of one (b, h) and two CTAs share an SM.  Windows are short -- ten
+// One CTA takes 128 query rows -- tokens of one (b, h), or fewer tokens of 2, 4, .. heads that share a
+// key head -- and two CTAs share an SM.  Windows are short -- ten
 // to forty blocks of 128 -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue
 // would be a large share of its life if nothing ran beside them; with two independent CTAs one's
 // softmax, start and end overlap the other's matrix products, and a tile visits its own key
@@ -158,6 +159,22 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
+// The rows of a tile: 2^lg heads that share a key head, and 128 / 2^lg tokens.
+struct Rows {
+  int first, b, h0, lg;  // row 0 is token `first` of head h0
+  __device__ __forceinline__ int token(int r) const { return first + (r >> lg); }
+  __device__ __forceinline__ int head(int r) const { return h0 + (r & ((1 << lg) - 1)); }
+  // the row's place among the D-element rows of a packed [B][Sq][H][D] tensor, from row 0's on
+  __device__ __forceinline__ size_t base(const WindowCall& c) const { return (size_t(b) * c.Sq + first) * c.H + h0; }
+  __device__ __forceinline__ unsigned place(const WindowCall& c, int r) const {
+    return unsigned(r + (r >> lg) * (c.H - (1 << lg)));
+  }
+  // its LSE (of the last token past the end)
+  __device__ __forceinline__ size_t lse(const WindowCall& c, int r) const {
+    return (size_t(b) * c.H + head(r)) * c.Sq + min(token(r), c.Sq - 1);
+  }
+};
+
 // What becomes of a tile's result.
 enum Result : int {
   kWrite = 0,       // written
@@ -199,7 +216,7 @@ __device__ __forceinline__ RowEnd finish_row(float m, float l, float la, bool in
 // memory, added in the order of the parts.  16 remote reads of 16 bytes a lane are in flight.
 template <int D, bool kOutF32, int kResult, int N>
 __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluster_group& cluster, uint8_t* smem,
-                                           int q_first, int b, int h) {
+                                           const Rows& rows) {
   constexpr bool kAcc = kResult != kWrite;
   constexpr int kShare = kBlockM / N / 4;  // rows of a warp
   constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes, kRows = 16 / N;  // of a row; of an instruction; in flight
@@ -208,8 +225,9 @@ __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluste
   float* ml = reinterpret_cast<float*>(smem + Geometry<D>::kOffParts);
   float w[N], l = 0.f, la = 0.f, m = -INFINITY;  // of row r0 + lane
   const int mine = r0 + min(lane, kShare - 1);
-  const bool in_range = q_first + mine < c.Sq;
-  const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + (in_range ? q_first + mine : 0);
+  const bool in_range = rows.token(mine) < c.Sq;
+  const size_t lse_idx = rows.lse(c, mine);
+  const unsigned place = in_range ? rows.place(c, mine) : 0u;  // past the end any row may be read
   if (kAcc) la = c.lse[lse_idx];
   float lk[N];
 #pragma unroll
@@ -218,8 +236,7 @@ __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluste
     lk[k] = *cluster.map_shared_rank(ml + kBlockM + mine, k);
   }
   const int sub = lane / kLanes, vec = lane % kLanes;
-  const size_t out_at = ((size_t(b) * c.Sq + q_first + r0 + sub) * c.H + h) * size_t(D) + 4 * vec;
-  const size_t step = size_t(kAtOnce) * c.H * D;
+  const size_t out_base = rows.base(c) * D + 4 * vec;
   RowEnd end;
 #pragma unroll
   for (int s0 = 0; s0 < kShare / kAtOnce; s0 += kRows) {
@@ -232,18 +249,15 @@ __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluste
 #pragma unroll
       for (int k = 0; k < N; ++k) x[s][k] = *cluster.map_shared_rank(part, k);
       if constexpr (kAcc) {
-        run[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q_first + r < c.Sq) {
-          const size_t at = out_at + (s0 + s) * step;
-          if constexpr (kResult == kMergeFrom32) {
-            run[s] = *reinterpret_cast<const float4*>(c.o_run + at);
-          } else if constexpr (kOutF32) {
-            run[s] = *reinterpret_cast<const float4*>(static_cast<const float*>(c.out) + at);
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(c.out) + at);
-            run[s] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
-          }
+        const size_t at = out_base + size_t(__shfl_sync(0xffffffffu, place, kAtOnce * (s0 + s) + sub)) * D;
+        if constexpr (kResult == kMergeFrom32) {
+          run[s] = *reinterpret_cast<const float4*>(c.o_run + at);
+        } else if constexpr (kOutF32) {
+          run[s] = *reinterpret_cast<const float4*>(static_cast<const float*>(c.out) + at);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(c.out) + at);
+          run[s] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
         }
       }
     }
@@ -277,7 +291,7 @@ __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluste
         o.z = fmaf(wk, x[s][k].z, o.z), o.w = fmaf(wk, x[s][k].w, o.w);
       }
       const int live = __shfl_sync(0xffffffffu, int(end.write), i);
-      const size_t at = out_at + (s0 + s) * step;
+      const size_t at = out_base + size_t(__shfl_sync(0xffffffffu, place, i)) * D;
       if (live) {
         if constexpr (kOutF32) *reinterpret_cast<float4*>(static_cast<float*>(c.out) + at) = o;
         else
@@ -292,7 +306,7 @@ template <int D, bool kOutF32, int kResult, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2)
     window_sm100_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowCall c,
-                        const __grid_constant__ CUtensorMap tm_o, float scale_log2, float rescale_log2,
+                        const __grid_constant__ CUtensorMap tm_o, int lg, float scale_log2, float rescale_log2,
                         int* err, long long wait_limit) {
   using G = Geometry<D>;
   constexpr bool kAcc = kResult != kWrite;
@@ -308,11 +322,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   // against 100; 44160 x 16, where a head alone fills the GPU, 1450 against 1462
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = kSplit ? int(cluster.block_rank()) : 0, n_ranks = kSplit ? int(cluster.num_blocks()) : 1;
-  const unsigned n_heads = unsigned(c.H) * unsigned(c.B), item = blockIdx.x / unsigned(n_ranks);
+  const unsigned n_heads = unsigned(c.H >> lg) * unsigned(c.B), item = blockIdx.x / unsigned(n_ranks);
   const int tile = int((gridDim.x / unsigned(n_ranks) - 1 - item) / n_heads);
   const int bh = int(item % n_heads);
-  const int b = bh / c.H, h = bh - b * c.H;
-  const int q_first = tile * kBlockM;
+  const int b = bh / (c.H >> lg), h = (bh - b * (c.H >> lg)) << lg;
+  const int n_tokens = kBlockM >> lg, q_first = tile * n_tokens;
+  const Rows rows{q_first, b, h, lg};
   volatile int* abort_flag = &bars.abort;
 
   if (warp == kWarpProducer) {
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_release();
   const int len = sequence_length(c, b);
   const int off = c.from_end ? len - c.Sq : c.off;
-  const int last_row = min(q_first + kBlockM, c.Sq) - 1;
+  const int last_row = min(q_first + n_tokens, c.Sq) - 1;  // a token, as q_first
   const Blocks blk = tile_blocks(c, off + q_first, off + last_row, len, rank, n_ranks);
   // The first loads go out before the block meets: nothing waits on their barriers earlier, and
   // their latency covers the rest of the set-up.
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t t_s = tmem + lane_bits;
     const uint32_t t_o = tmem + lane_bits + 2 * kBlockN;
     const uint32_t bar_s0 = smem_u32(&bars.s_full[0]), bar_p0 = smem_u32(&bars.p_full[0]);
-    const int q = q_first + row;
+    const int q = rows.token(row);
     const bool in_range = q < c.Sq;
     const KeyRange r = visible_keys(off + min(q, c.Sq - 1), c.left, c.right, c.sinks, len);
     // keys that every row of the tile sees: blocks inside need no mask
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ------------------------------------------------------------------ epilogue
-    const size_t lse_idx = (size_t(b) * c.H + h) * c.Sq + (in_range ? q : 0);
+    const size_t lse_idx = rows.lse(c, row);
     // Results other than a bf16 tile that leaves by TMA go through shared memory, so that a warp reads
     // 16 bytes a lane of whole rows of the running O, kBatch instructions at a time, and writes whole
     // rows.  (Each thread on its own row: 32 rows an instruction, and a read before every write.)
@@ -500,14 +515,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kCols = kRun32 ? 4 : 8, kLanes = D / kCols;  // of a lane; of a row
     constexpr int kAtOnce = 32 / kLanes, kSteps = 32 / kAtOnce, kBatch = kSteps < 16 ? kSteps : 16;
     const int sub = lane / kLanes, col = kCols * (lane % kLanes);
-    const int warp_first = q_first + warp * 32;
-    const size_t out_at = ((size_t(b) * c.Sq + warp_first + sub) * c.H + h) * size_t(D) + col;
-    const size_t step = size_t(kAtOnce) * c.H * D;
-    auto running = [&](int s) {  // the lane's columns of row kAtOnce s + sub
-      if (warp_first + kAtOnce * s + sub >= c.Sq) return make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (kResult == kMergeFrom32) return *reinterpret_cast<const uint4*>(c.o_run + out_at + s * step);
-      else if constexpr (kOutF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(c.out) + out_at + s * step);
-      else return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.out) + out_at + s * step);
+    // past the end any row may be read: it is not used
+    const unsigned place = in_range ? rows.place(c, row) : 0u;
+    const size_t out_base = rows.base(c) * D + col;
+    auto row_at = [&](int s) {  // the lane's columns of the warp's row kAtOnce s + sub
+      return out_base + size_t(__shfl_sync(0xffffffffu, place, kAtOnce * s + sub)) * D;
+    };
+    auto running = [&](int s) {
+      const size_t at = row_at(s);
+      if constexpr (kResult == kMergeFrom32) return *reinterpret_cast<const uint4*>(c.o_run + at);
+      else if constexpr (kOutF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(c.out) + at);
+      else return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.out) + at);
     };
     uint4 run[kAcc ? kBatch : 1];
     float la = 0.f;
@@ -617,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
             const int live = __shfl_sync(0xffffffffu, int(write), r);
-            const size_t at = out_at + (s0 + s) * step;
+            const size_t at = row_at(s0 + s);
             if (live) {
               if constexpr (kOutF32)
                 *reinterpret_cast<float4*>(static_cast<float*>(c.out) + at) = make_float4(o[0], o[1], o[2], o[3]);
@@ -779,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // fold the parts: each block finishes 128 / n_ranks rows, the sums in the order of the parts
     cluster.sync();
     if (warp < 4) {
-      if (n_ranks == 2) fold_parts<D, kOutF32, kResult, 2>(c, cluster, smem, q_first, b, h);
-      else if (n_ranks == 4) fold_parts<D, kOutF32, kResult, 4>(c, cluster, smem, q_first, b, h);
-      else fold_parts<D, kOutF32, kResult, 8>(c, cluster, smem, q_first, b, h);
+      if (n_ranks == 2) fold_parts<D, kOutF32, kResult, 2>(c, cluster, smem, rows);
+      else if (n_ranks == 4) fold_parts<D, kOutF32, kResult, 4>(c, cluster, smem, rows);
+      else fold_parts<D, kOutF32, kResult, 8>(c, cluster, smem, rows);
     }
     cluster.sync();  // no block leaves while another reads its shared memory
   }
@@ -792,15 +810,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-// [B][S][H][D] bf16 tensor whose tokens are `stride` elements apart: 64 columns x 1 head x
-// `rows` tokens x 1 batch, 128-byte swizzle; rows past S read as 0.
-bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long long stride, unsigned rows) {
+// [B][S][H][D] bf16 tensor whose tokens are `stride` elements apart: 64 columns x `heads` heads x
+// `tokens` tokens x 1 batch, 128-byte swizzle; tokens past S read as 0.
+bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long long stride, unsigned tokens,
+            unsigned heads) {
   auto fn = tensor_map_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(S), cuuint64_t(B)};
   const cuuint64_t token = cuuint64_t(stride) * 2;
   const cuuint64_t strides[3] = {cuuint64_t(D) * 2, token, B > 1 ? token * cuuint64_t(S) : token};
-  const cuuint32_t box[4] = {64, 1, rows, 1};
+  const cuuint32_t box[4] = {64, heads, tokens, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -813,16 +832,31 @@ bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long 
 // every SM.  Measured, parts 1 / 2 / 4 / 8: 20 tiles of 512 keys 9.9 / 9.2 / 7.9 / 10.3 us, of 2048
 // 25.8 / 17.5 / 12.6 / 14.1; 100 tiles of 1024 15.7 / 16.2 (200 blocks), of 4096 47.6 / 38.2; 48 tiles of
 // 2048 26.5 / 18.5 / 18.1; 37 tiles of 512 10.1 / 9.4 / 10.7 / 16.9.
+// Heads of a key head that a tile takes together, as a power of two.  Tokens then span fewer keys and
+// few of them still fill a tile: 16000 x 32 heads on 8, causal window 2000, 579 -> 530 us, 4000 x 32 on
+// 8, window 100, 40 -> 34.5; 16 tokens of 8 sequences x 32 heads on 8 against 4096 keys 77 -> 35.
+int heads_log2(const WindowCall& c) {
+  int lg = 0;
+  while (lg < 7 && (c.H / c.Hkv) % (2 << lg) == 0) ++lg;
+  return lg;
+}
+
+long long tiles(const WindowCall& c, int lg) {
+  const int n = kBlockM >> lg;
+  return ((long long)c.Sq + n - 1) / n * (c.H >> lg) * c.B;
+}
+
 struct Plan {
   int parts;
   double us;
 };
 
 Plan plan(const WindowCall& c) {
-  const long long items = (long long)((c.Sq + kBlockM - 1) / kBlockM) * c.H * c.B, sms = sm_count();
+  const int lg = heads_log2(c);
+  const long long items = tiles(c, lg), sms = sm_count(), span = kBlockM >> lg;
   long long keys = c.Skv, early = 0;  // of a tile, at most
-  if (c.left >= 0 && c.right >= 0 && (long long)c.left + c.right + kBlockM < keys) {
-    keys = (long long)c.left + c.right + kBlockM;
+  if (c.left >= 0 && c.right >= 0 && c.left + c.right + span < keys) {
+    keys = c.left + c.right + span;
     early = c.sinks < c.Skv - keys ? c.sinks : c.Skv - keys;
   }
   const long long blocks = (keys + kBlockN - 1) / kBlockN + (early + kBlockN - 1) / kBlockN;
@@ -843,8 +877,9 @@ cudaError_t launch_parts(const WindowCall& c, int n_ranks, const CUtensorMap& tq
   static SmemOptIn opt_in;
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), Geometry<D>::kSmem);
   if (e != cudaSuccess) return e;
+  const int lg = heads_log2(c);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((c.Sq + kBlockM - 1) / kBlockM) * unsigned(c.H) * unsigned(c.B) * unsigned(n_ranks));
+  cfg.gridDim = dim3(unsigned(tiles(c, lg) * n_ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Geometry<D>::kSmem;
   cfg.stream = stream;
@@ -857,7 +892,7 @@ cudaError_t launch_parts(const WindowCall& c, int n_ranks, const CUtensorMap& tq
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kSplit ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, to,
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, c, to, lg,
                             float(double(c.scale) * 1.4426950408889634074),
                             kRescaleLog2, err, kDefaultWaitLimit);
 }
@@ -886,15 +921,17 @@ cudaError_t launch_d(const WindowCall& c, const CUtensorMap& tq, const CUtensorM
 double window_sm100_us(const WindowCall& c) { return plan(c).us; }
 
 cudaError_t launch_window_sm100(const WindowCall& c, int* err, cudaStream_t stream) {
+  const int lg = heads_log2(c);
   CUtensorMap tq, tk, tv, to;
-  if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM)) return cudaErrorInvalidValue;
+  if (!encode(&tq, c.q, c.B, c.Sq, c.H, c.D, c.q_stride, kBlockM >> lg, 1u << lg)) return cudaErrorInvalidValue;
   if (c.Skv == 0) tk = tv = tq;  // no block loads through them
-  else if (!encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN) ||
-           !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kBlockN))
+  else if (!encode(&tk, c.k, c.B, c.Skv, c.Hkv, c.D, c.k_stride, kBlockN, 1) ||
+           !encode(&tv, c.v, c.B, c.Skv, c.Hkv, c.D, c.v_stride, kBlockN, 1))
     return cudaErrorInvalidValue;
   // bf16 results leave by TMA; the other forms do not use the map
   if (c.out_f32 || c.accumulate) to = tq;
-  else if (!encode(&to, c.out, c.B, c.Sq, c.H, c.D, (long long)c.H * c.D, kBlockM)) return cudaErrorInvalidValue;
+  else if (!encode(&to, c.out, c.B, c.Sq, c.H, c.D, (long long)c.H * c.D, kBlockM >> lg, 1u << lg))
+    return cudaErrorInvalidValue;
   return c.D == 128 ? launch_d<128>(c, tq, tk, tv, to, err, stream) : launch_d<64>(c, tq, tk, tv, to, err, stream);
 }
 

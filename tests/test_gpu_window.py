@@ -282,6 +282,33 @@ def test_tiles_and_parts_in_every_form_of_result(B, H, Hkv, Sq, Skv, D, w):
         check(out, lse, ref, q, k, D ** -0.5, merges=3)
 
 
+@pytest.mark.parametrize("H,Hkv", [(2, 1), (8, 2), (12, 2), (24, 2), (64, 1), (128, 1), (256, 1), (20, 1), (27, 3)])
+@pytest.mark.parametrize("B,Sq,Skv,D", [(1, 1, 300, 128), (2, 5, 700, 64), (1, 37, 90, 64), (1, 130, 260, 128)])
+def test_heads_that_share_a_tile(H, Hkv, B, Sq, Skv, D):
+    q, k, v = make(30 + H + Sq, B, H, Hkv, Sq, Skv, D)
+    at, w = Skv - Sq, dict(left=60, right=2, sinks=3)
+    kv_len = [Skv] + [Skv // 3] * (B - 1)
+    for dt in (torch.bfloat16, torch.float32):
+        run_window(q, k, v, q_pos=at, kv_len=kv_len, out_dtype=dt, **w)
+    wide = torch.cat([torch.full_like(q[:, :, :1], float("nan")), q, torch.full_like(q[:, :, :1], float("nan"))], 2).to(DEV)
+    cut = Skv // 2
+    ref = ow.window_attention(q, k, v, D ** -0.5, q_pos=at, **w)
+    pad = 8 * D
+    for acc_dtype in (None, torch.bfloat16, torch.float32):  # guarded outputs, q inside a wider row
+        n = q.numel()
+        buf = torch.full((n + 2 * pad,), 7.0, dtype=torch.bfloat16 if acc_dtype is None else acc_dtype, device=DEV)
+        out = buf[pad:-pad].view(q.shape)
+        run = torch.empty(q.shape, device=DEV) if acc_dtype is None else out
+        lse = torch.empty((B, H, Sq), device=DEV)
+        qd, kd, vd = wide[:, :, 1:-1], k.to(DEV), v.to(DEV)
+        cp.window_fwd(qd, kd[:, :cut].contiguous(), vd[:, :cut].contiguous(), out=run, lse=lse, q_pos=at, **w)
+        cp.window_fwd(qd, kd[:, cut:].contiguous(), vd[:, cut:].contiguous(), out=out, lse=lse, accumulate=True,
+                      run=run if acc_dtype is None else None, q_pos=at, k_pos=cut, **w)
+        torch.cuda.synchronize()
+        check(out, lse, ref, q, k, D ** -0.5, merges=2)
+        assert (buf[:pad] == 7).all() and (buf[-pad:] == 7).all()
+
+
 def test_merge_into_rows_that_hold_anything():
     # running rows with LSE = -inf are never used, whatever they hold; rows that see nothing stay
     for B, H, Sq, Skv in ((1, 2, 200, 900), (2, 20, 500, 300)):
