@@ -509,7 +509,7 @@ CPATTN_API int cpattn_seq2head_qkv_norm_rope(const void* q, const void* k, const
  * cpattn_call -- one of the five calls above with its arguments as `n` words of 8 bytes, in their
  * order: pointers and integers as 64-bit integers, floats as the bits of a double, the stream
  * last.  For bindings of languages that pay for every argument of a foreign call (21 of them cost
- * Python 3 us, more than the launch).  Errors: those of the call; CPATTN_ERR_SHAPE for an unknown
+ * Python about 3 us).  Errors: those of the call; CPATTN_ERR_SHAPE for an unknown
  * entry, another number of words, or a word that an int cannot hold; CPATTN_ERR_NULL without words.
  */
 typedef enum {
