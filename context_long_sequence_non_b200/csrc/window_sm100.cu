@@ -93,6 +93,9 @@ struct Geometry {
   static constexpr int kOffParts = kBlockM * D * 4;  // behind a staged O: its rows' m and l
   static_assert(kOffParts + kBlockM * 8 <= kOffBars);
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  // A third would wait on its SM for TMEM that a CTA of another cluster holds while that cluster waits
+  // for a CTA behind it.
+  static_assert(3 * (kSmem + 1024) > 228 * 1024, "no more than two CTAs per SM");
 };
 
 struct __align__(8) Barriers {

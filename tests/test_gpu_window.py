@@ -605,3 +605,59 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (o, l), (ro, rl) in got:
         assert torch.equal(o, ro) and torch.equal(l, rl)
+
+
+def _mixed_calls():
+    """Calls that share tiles out to clusters, in every kernel, and ones that fill the GPU."""
+    def call(fn, *shapes, dtype=torch.bfloat16, **kw):
+        g = torch.Generator().manual_seed(31 + len(shapes[0]) + shapes[1][1])
+        ts = [torch.randn(*s, generator=g).to(dtype).to(DEV) for s in shapes]
+        return ts, lambda: fn(*ts, **kw)
+    kv = lambda B, S, H, D: ((B, S, H, D), (B, S, H, D))
+    return [call(cp.window_fwd, (1, 300, 2, 128), *kv(1, 3000, 2, 128), left=-1, right=-1),
+            call(cp.window_fwd, (1, 200, 8, 64), *kv(1, 2100, 2, 64), left=1500, right=0, q_pos=1900, sinks=9),
+            call(cp.window_fwd, (1, 90, 3, 96), *kv(1, 1000, 3, 96), dtype=torch.float32, left=-1, right=-1),
+            call(cp.window_decode, (2, 1, 16, 128), *kv(2, 3100, 4, 128), left=2500),
+            call(cp.window_decode, (1, 1, 4, 64), *kv(1, 2200, 4, 64), dtype=torch.float32),
+            call(cp.window_decode, (2, 64, 8, 128), *kv(2, 2300, 4, 128), left=2000),
+            call(cp.window_fwd, (1, 1300, 24, 128), *kv(1, 1400, 24, 128), left=300, right=20, q_pos=50),
+            call(cp.fwd, (1, 700, 8, 128), *kv(1, 900, 8, 128))]
+
+
+def test_clustered_calls_beside_one_another():
+    calls = _mixed_calls()
+    want = [f() for _, f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for turn in range(6):
+        got = []
+        for i in range(len(calls)):
+            with torch.cuda.stream(streams[(i + turn) % len(streams)]):
+                got.append([calls[i][1]() for _ in range(3)])
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            for o, l in g:
+                assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_clustered_calls_in_two_graphs():
+    calls = _mixed_calls()
+    graphs, outs = [], []
+    for order in (calls, calls[::-1]):  # captured twice, replayed beside one another
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([f() for _, f in order])
+        graphs.append(g)
+    for seed in range(2):
+        for ts, _ in calls:
+            for t in ts:
+                t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)))
+        want = [f() for _, f in calls]
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        for got, ref in ((outs[0], want), (outs[1], want[::-1])):
+            for (o, l), (ow_, lw) in zip(got, ref):
+                assert torch.equal(o, ow_) and torch.equal(l, lw)
