@@ -15,9 +15,9 @@
 // holds both elements of its pairs in either layout, so the rotation needs no exchange; the norm
 // is one shuffle reduction over a row's lanes.  Loads run ahead through a small cp.async ring per
 // warp, across heads and tokens, so the angles' latency and the stores hide behind them (plain
-// register loads, four rows at a time, took 73 us where this takes 61).  Frequencies and weights
-// sit in shared memory.  Measured on a B200: 44160 tokens x 16 heads of 128, three axes, 61 us
-// (5.9 TB/s, 90% of the measured copy rate); norm + rotation + re-partition of Q, K and V of the
+// register loads, four rows at a time, took 73 us where this took 61).  Frequencies and weights
+// sit in shared memory.  Measured on a B200: 44160 tokens x 16 heads of 128, three axes, 60 us
+// (6.0 TB/s, 92% of the measured copy rate); norm + rotation + re-partition of Q, K and V of the
 // same size 180 us (6.0 TB/s, 92%).  rope_rows_kernel takes every other shape, an element at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -284,14 +284,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __gr
     const int pos = next_pos;
     if (item + n_warps < n_items) next_pos = position(item + n_warps);
     __syncwarp();  // the previous token's angles are read no more
-    for (int p0 = 0; p0 < half; p0 += 32) {
-      const int p = p0 + lane;
-      double angle = 0.0;
+    // two pairs a lane at a time: the chain of one (64-bit products, conversions, sine and cosine) is long
+    int p0 = 0;
+    for (; p0 + 32 < half; p0 += 64) {
+      const int pa = p0 + lane, pb = min(pa + 32, half - 1);
+      double xa = 0.0, xb = 0.0;
       for (int a = 0; a < c.n_axes; ++a) {
-        const int at = __shfl_sync(0xffffffffu, pos, a);
-        if (p < half) angle = fma(double(at), freq_sh[a * half + p], angle);
+        const double at = __shfl_sync(0xffffffffu, pos, a);
+        xa = fma(at, freq_sh[a * half + pa], xa);
+        xb = fma(at, freq_sh[a * half + pb], xb);
       }
-      if (p < half) cs[p] = turn_by(angle, c.factor);
+      const float2 ca = turn_by(xa, c.factor), cb = turn_by(xb, c.factor);
+      cs[pa] = ca;
+      cs[pb] = cb;
+    }
+    if (p0 < half) {
+      const int p = min(p0 + lane, half - 1);
+      double x = 0.0;
+      for (int a = 0; a < c.n_axes; ++a) x = fma(double(__shfl_sync(0xffffffffu, pos, a)), freq_sh[a * half + p], x);
+      cs[p] = turn_by(x, c.factor);
     }
     __syncwarp();
     // cos and sin of this lane's pairs: 8 l + i (halves), or 4 (va / 8) + i and 4 (vb / 8) + i
@@ -336,10 +347,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float4 p = ga[i], q = gb[i];
-              a[2 * i] = fmul2(fmul2(fmul2(a[2 * i], r2), make_float2(p.x, p.y)), os);
-              a[2 * i + 1] = fmul2(fmul2(fmul2(a[2 * i + 1], r2), make_float2(p.z, p.w)), os);
-              b[2 * i] = fmul2(fmul2(fmul2(b[2 * i], r2), make_float2(q.x, q.y)), os);
-              b[2 * i + 1] = fmul2(fmul2(fmul2(b[2 * i + 1], r2), make_float2(q.z, q.w)), os);
+              a[2 * i] = fmul2(fmul2(a[2 * i], r2), make_float2(p.x, p.y));
+              a[2 * i + 1] = fmul2(fmul2(a[2 * i + 1], r2), make_float2(p.z, p.w));
+              b[2 * i] = fmul2(fmul2(b[2 * i], r2), make_float2(q.x, q.y));
+              b[2 * i + 1] = fmul2(fmul2(b[2 * i + 1], r2), make_float2(q.z, q.w));
+            }
+            if (c.out_scale != 1.f) {  // (times 1 changes nothing)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = fmul2(a[i], os), b[i] = fmul2(b[i], os);
             }
           }
           if (turns && rotate) {
@@ -350,11 +365,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __gr
                 a[i] = ffma2(x, make_float2(wa.x, wa.x), fmul2(make_float2(x.y, x.x), make_float2(-wa.y, wa.y)));
                 b[i] = ffma2(y, make_float2(wb.x, wb.x), fmul2(make_float2(y.y, y.x), make_float2(-wb.y, wb.y)));
               } else {  // pairs 2i and 2i + 1: a cos - b sin, b cos + a sin
-                const float2 x = a[i], y = b[i];
-                const float2 co = make_float2(w[2 * i].x, w[2 * i + 1].x);
-                const float2 si = make_float2(w[2 * i].y, w[2 * i + 1].y);
-                a[i] = ffma2(x, co, fmul2(y, make_float2(-si.x, -si.y)));
-                b[i] = ffma2(y, co, fmul2(x, si));
+                const float2 x = a[i], y = b[i], w0 = w[2 * i], w1 = w[2 * i + 1];
+                a[i] = make_float2(fmaf(x.x, w0.x, -(y.x * w0.y)), fmaf(x.y, w1.x, -(y.y * w1.y)));
+                b[i] = make_float2(fmaf(y.x, w0.x, x.x * w0.y), fmaf(y.y, w1.x, x.y * w1.y));
               }
             }
           }
@@ -379,12 +392,24 @@ cudaError_t launch_vector(const RopeCall& c, int max_heads, cudaStream_t stream)
   int lanes_log2 = 0;
   while ((1 << lanes_log2) < c.D / 16) ++lanes_log2;
   const int rows_per_warp = 32 >> lanes_log2;
-  // few tokens: several warps share a token's heads (each with its own angles), down to one
-  // warp-load of heads each, until every SM has a block.  Splitting further costs more in angles than
-  // it hides: 1000 tokens x 32 heads 6.3 us, and 10.9 with twice as many warps as the aim.
-  const long long want = (long long)sm_count() * kWarpsPerBlock;
+  // Warps that share a token's heads, each with its own angles: as many as give the fewest steps to the
+  // warp with the most, an item's angles counted as 2.5 steps.  Measured, parts 1 / 2 / 4: 1000 tokens
+  // x 32 heads - / 6.1 / 9.1 us, 2000 10.2 / 11.6 / 14, 3000 17.5 / 16.2 / 23, 5000 22.4 / 22.8 / 34, 8000
+  // 31.5 / 32.3 / 51.
+  const long long warps = (long long)sm_count() * kBlocksPerSm * kWarpsPerBlock;
   int parts_log2 = 0;
-  while ((long long)c.tokens << parts_log2 < want && rows_per_warp << parts_log2 < max_heads) ++parts_log2;
+  double least = 0.0;
+  for (int p = 0; p == 0 || rows_per_warp << (p - 1) < max_heads; ++p) {
+    const long long items = (long long)c.tokens << p;
+    if (p > 0 && items > 1 << 30) break;
+    double steps = 2.5;
+    for (int t = 0; t < c.n_tensors; ++t) {
+      const int heads = (c.t[t].heads + (1 << p) - 1) >> p;
+      steps += (heads + rows_per_warp - 1) / rows_per_warp;
+    }
+    const double cost = double((items + warps - 1) / warps) * steps;
+    if (p == 0 || cost < least) least = cost, parts_log2 = p;
+  }
   const long long blocks = (((long long)c.tokens << parts_log2) + kWarpsPerBlock - 1) / kWarpsPerBlock;
   const long long cap = (long long)sm_count() * kBlocksPerSm;
   cudaLaunchConfig_t cfg = {};

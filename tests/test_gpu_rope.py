@@ -139,6 +139,25 @@ def test_qk_norm_rope(T, Hq, Hk, D, rot, interleaved, dtype):
     assert torch.equal(row[:, Hq + Hk:].cpu(), q)  # the other heads of the row are left alone
 
 
+# a token's heads in 8, 4, 2 and 1 parts, uneven ones among them; three blocks of 32 pairs and a half one
+@pytest.mark.parametrize("T,Hq,Hk,D,rot", [(150, 35, 5, 128, 128), (420, 32, 8, 64, 64), (900, 9, 3, 128, 96),
+                                           (1100, 70, 1, 80, 80), (3000, 24, 8, 128, 128), (2500, 5, 3, 256, 224)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_parts_of_a_token(T, Hq, Hk, D, rot, interleaved):
+    q, k = randn(T, T, Hq, D, sigma=3.0), randn(T + 1, T, Hk, D, sigma=0.1)
+    gq, gk = 1 + 0.1 * randn(1, D, dtype=torch.float32), 1 + 0.1 * randn(2, D, dtype=torch.float32)
+    pos = torch.arange(T, dtype=torch.int32) * 17 - 900
+    freq, _ = cp.rope_frequencies(rot)
+    out = cp.qk_norm_rope(q.to(DEV), k.to(DEV), gq.to(DEV), gk.to(DEV), pos.to(DEV), freq.to(DEV),
+                          interleaved=interleaved)
+    plain = cp.rope(q.to(DEV), pos.to(DEV), freq.to(DEV), interleaved=interleaved)
+    torch.cuda.synchronize()
+    for x, g, got in ((q, gq, out[0]), (k, gk, out[1])):
+        n = ow.rms_norm(x, g, 1e-6, 1.0)
+        check(got, ow.rotate(n, pos.numpy(), freq, interleaved, 1.0), n, rot, interleaved, 1.0)
+    check(plain, ow.rotate(q, pos.numpy(), freq, interleaved, 1.0), _f64(q), rot, interleaved, 1.0)
+
+
 @pytest.mark.parametrize("P,S_l,H,D,rot", [(2, 3, 4, 64, 64), (4, 33, 8, 128, 128), (8, 17, 16, 128, 64), (1, 9, 4, 256, 256),
                                            (3, 7, 6, 80, 48), (2, 11, 24, 72, 20), (2, 300, 4, 32, 32)])
 @pytest.mark.parametrize("norm", [True, False])
