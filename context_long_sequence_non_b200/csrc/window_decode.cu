@@ -272,7 +272,9 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
   // they crowded some SMs (8 sequences of 4 tokens, calls back to back: 15.1 us against 13.3).
   griddep_release();
 
-  // ---- fold the warps' partials: m and l first, then O scaled to the block's maximum
+  // ---- fold the warps' partials: m and l first, then O scaled to the block's maximum.  A row's keys are
+  // told by l, 0 without any and 1 or more with some: m is -inf for NaN scores too, which the maximum
+  // drops, and their NaN l and O are to reach the result
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][r]);
-    const float w = m[hh] == -INFINITY ? 0.f : ex2(m[hh] - top);
+    const float w = l[hh] == 0.f ? 0.f : ex2(m[hh] - top);
     if (r < n_rows) {
 #pragma unroll
       for (int t = 0; t < D / 8; ++t)
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < kWarps; ++v)
-        sum += part_m[v][r] == -INFINITY ? 0.f : part_l[v][r] * ex2(part_m[v][r] - top);
+        sum += part_l[v][r] == 0.f ? 0.f : part_l[v][r] * ex2(part_m[v][r] - top);
       cta_m[r] = top;
       cta_l[r] = sum;
     }
@@ -344,11 +346,11 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) {
-      const float w = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - top);  // 0: that block saw no key
+      const float w = lk[k] == 0.f ? 0.f : ex2(mk[k] - top);  // 0: that block saw no key
       sum = fmaf(w, lk[k], sum);
       a.x = fmaf(w, xk[k].x, a.x), a.y = fmaf(w, xk[k].y, a.y), a.z = fmaf(w, xk[k].z, a.z), a.w = fmaf(w, xk[k].w, a.w);
     }
-    const float inv = top == -INFINITY ? 0.f : 1.0f / sum;  // no visible key: O = 0, LSE = -inf
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // no visible key: O = 0, LSE = -inf
     const int row = row0 + r, i = row / G, h = kvh * G + (row - i * G);
     const long long at = (((long long)b * c.Sq + i) * c.H + h) * D + d;
     if constexpr (kOutF32)
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kWarps * 32, Decode<D>::kCtas)
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.out) + at) =
           make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (d == 0 && c.lse != nullptr)
-      c.lse[((long long)b * c.H + h) * c.Sq + i] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+      c.lse[((long long)b * c.H + h) * c.Sq + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
   if (n_ranks > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }

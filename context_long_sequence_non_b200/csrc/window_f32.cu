@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) window_f32_kernel
       for (int g = 0; g < kPairs; ++g) o[i][g] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kMaxCluster; ++k) {
-        const float w = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - m[i]);  // 0: that block saw no key
+        const float w = lk[k] == 0.f ? 0.f : ex2(mk[k] - m[i]);  // 0: that block saw no key
         l[i] = fmaf(w, lk[k], l[i]);
 #pragma unroll
         for (int g = 0; g < kPairs; ++g) o[i][g] = ffma2(make_float2(w, w), x[k][g], o[i][g]);
@@ -305,7 +305,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) window_f32_kernel
   for (int i = 0; i < R; ++i) {
     const int r = row0 + i;
     if (r >= n_rows || r % n_ranks != rank) continue;
-    const bool empty = m[i] == -INFINITY;  // no visible key: O = 0, LSE = -inf
+    // No visible key: O = 0, LSE = -inf.  (Told by l, 1 or more with some: m is -inf for NaN scores too,
+    // which the maximum drops, and their NaN l and O are the result.)
+    const bool empty = l[i] == 0.f;
     const float inv = empty ? 0.f : 1.0f / l[i];
     const int t = token(r), h = kvh * G + (q0 + r - t * G);
     const long long at = (((long long)b * c.Sq + t) * c.H + h) * c.D;

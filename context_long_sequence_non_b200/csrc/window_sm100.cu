@@ -186,7 +186,9 @@ enum Result : int {
 };
 
 // What a row's sum over keys (reference m in units of log2, sum l) and, merging, the running row
-// (log-sum-exp la) come to: O = fa running + fc new.
+// (log-sum-exp la) come to: O = fa running + fc new.  l is 0 for a row that saw no key and 1 or more for
+// one that did; m does not tell them apart, since it is -inf for NaN scores too (maxima drop them), whose
+// NaN l and O are the result.
 struct RowEnd {
   float fa, fc, lse;
   bool write;
@@ -194,7 +196,7 @@ struct RowEnd {
 
 template <int kResult>
 __device__ __forceinline__ RowEnd finish_row(float m, float l, float la, bool in_range) {
-  const bool empty = m == -INFINITY;
+  const bool empty = l == 0.f;
   const float lc2 = m + log2f(l);
   RowEnd r{0.f, empty ? 0.f : 1.0f / l, empty ? -INFINITY : lc2 * kLn2, in_range};
   if constexpr (kResult != kWrite) {
@@ -269,7 +271,7 @@ __device__ __forceinline__ void fold_parts(const WindowCall& c, const cg::cluste
       for (int k = 0; k < N; ++k) m = fmaxf(m, w[k]);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        w[k] = w[k] == -INFINITY ? 0.f : ex2(w[k] - m);  // 0: that part saw no key
+        w[k] = lk[k] == 0.f ? 0.f : ex2(w[k] - m);  // 0: that part saw no key
         l = fmaf(w[k], lk[k], l);
       }
       end = finish_row<kResult>(m, l, la, in_range);
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ok) {
       tc_fence_after();
       const float l = (l0.x + l0.y) + (l1.x + l1.y);
-      const bool empty = m == -INFINITY;
+      const bool empty = l == 0.f;
       const RowEnd end = finish_row<kResult>(m, l, la, in_range);
       const float fa = end.fa, fc = kSplit ? 1.f : end.fc, lse_out = end.lse;
       const bool write = end.write;

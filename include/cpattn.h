@@ -379,7 +379,8 @@ CPATTN_API int cpattn_head2seq(const void* src, void* dst, int P, int S_local, i
  * with len(b) = Skv, or kv_len[b] clamped to 0..Skv.  right = 0 is causal; left = right = w is
  * a two-sided band; left < 0 and right < 0 lift the bound on that side.  Then
  *   lse[b,h,i] = ln sum_visible exp(scale q.k),  out = sum_visible exp(scale q.k - lse) v.
- * A row that sees no key gets out = 0 and lse = -inf.
+ * A row that sees no key gets out = 0 and lse = -inf; a NaN in q gives NaN in the out and lse of every
+ * row of it that sees a key.
  *
  * q : [B][Sq][H][D], k and v : [B][Skv][Hkv][D], H a multiple of Hkv: query head h uses key head
  *   h / (H / Hkv).  q_stride, k_stride, v_stride: elements between consecutive tokens, 0 for
