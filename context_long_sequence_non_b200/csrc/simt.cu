@@ -155,6 +155,10 @@ __device__ __forceinline__ void merge_vec_f32(const uint4& a, const uint4& b, fl
 
 constexpr int kMergeRowsPerThread = 4;  // independent row vectors in flight per thread
 
+// Is one of two partials not empty?  Each LSE is asked for itself: the maximum of a NaN and -inf is -inf,
+// and a NaN partial beside an empty one is to give NaN.
+__device__ __forceinline__ bool any_keys(float la, float lb) { return la != -INFINITY || lb != -INFINITY; }
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(
     const uint4* o_a, const float* lse_a, const uint4* o_b, const float* lse_b, uint4* o,
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(
     if (!live[u]) continue;
     const float mx = fmaxf(la[u], lb[u]);
     float wa = 0.f, wb = 0.f;
-    if (mx != -INFINITY) {
+    if (any_keys(la[u], lb[u])) {
       const float ea = expf(la[u] - mx), eb = expf(lb[u] - mx);
       const float tot = ea + eb;
       L[u] = mx + logf(tot);
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_rows_kernel(
       if (!live[u]) continue;
       const float mx = fmaxf(la[u], lb[u]);
       float wa = 0.f, wb = 0.f, L = -INFINITY;
-      if (mx != -INFINITY) {
+      if (any_keys(la[u], lb[u])) {
         // CUDA's fast intrinsics: the arguments are <= 0 and tot is in [1, 2], where their
         // errors (a few float ulps) stay far below the merge's fp32 / LSE tolerances; every
         // lane of a row computes the same weights
@@ -309,17 +313,20 @@ __global__ void __launch_bounds__(kMergeThreads) combine_kernel(
     const long long idx = (long long)row * vpr + v;
     float ls[kMaxSplit + 1];
     float mx = -INFINITY;
+    bool some = false;  // a term that is not empty; fmaxf drops NaN, so mx does not tell
     for (int t = 0; t < n; ++t) {
       ls[t] = part_lse[t * lse_stride + li];
       mx = fmaxf(mx, ls[t]);
+      some |= ls[t] != -INFINITY;
     }
     const float la = kAcc ? lse[li] : -INFINITY;
     mx = fmaxf(mx, la);
+    some |= la != -INFINITY;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
     float tot = 0.f;
-    if (mx != -INFINITY) {
+    if (some) {
       for (int t = 0; t <= n; ++t) {
         const float lt = t < n ? ls[t] : la;
         if (lt == -INFINITY) continue;  // an empty term contributes nothing (and is not read)
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(kMergeThreads) combine_kernel(
       }
       L = mx + logf(tot);
     }
-    const float inv = tot > 0.f ? 1.0f / tot : 0.f;
+    const float inv = some ? 1.0f / tot : 0.f;
     uint4 r;
     if (kBf16) {
       r.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);

@@ -281,7 +281,7 @@ CPATTN_API int cpattn_fwd_accumulate(const void* q, const void* k, const void* v
  * running result with the online softmax, Fig. 3):
  *   L = max(La, Lb) + ln(exp(La - max) + exp(Lb - max))
  *   O = exp(La - L) * Oa + exp(Lb - L) * Ob
- * Two empty partials (La = Lb = -inf) give O = 0, L = -inf (never NaN).
+ * Two empty partials (La = Lb = -inf) give O = 0, L = -inf (never NaN); a NaN partial gives NaN.
  *
  * o_a, o_b, o : [B][S][H][D] in `dtype` (BF16 or F32); math in fp32.
  * lse_a, lse_b, lse : [B][H][S] float32.

@@ -145,3 +145,39 @@ def test_windowed_ring_step(kw):
     w = dict(left=150, right=100, sinks=6, q_pos=300, **kw)
     got, want = cp.ring_attention(bad_q, ks, vs, **w), cp.ring_attention(q, ks, vs, **w)
     check(got, want, bad, torch.ones_like(bad))
+
+
+# ------------------------------------------------------------------ merges and folds
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (128, torch.float32), (96, torch.float32), (512, torch.float32)])
+def test_merge(D, dtype):
+    B, S, H = 2, 70, 3
+    g = torch.Generator().manual_seed(D)
+    o = [torch.randn(B, S, H, D, generator=g).to(dtype).to(DEV) for _ in range(2)]
+    l = [torch.randn(B, H, S, generator=g).to(DEV) for _ in range(2)]
+    for t, part in enumerate((slice(0, 20), slice(20, 40))):  # NaN on one side, nothing on the other
+        o[t][:, part], l[t][:, :, part] = NAN, NAN
+        o[1 - t][:, part], l[1 - t][:, :, part] = 0, -math.inf
+    o[0][:, 40:45], l[0][:, :, 40:45] = NAN, NAN  # beside an ordinary part
+    for t in range(2):  # nothing on both
+        o[t][:, 45:50], l[t][:, :, 45:50] = 0, -math.inf
+    out, lse = cp.merge(o[0], l[0], o[1], l[1])
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:, :45]).all() and torch.isnan(lse[:, :, :45]).all()
+    assert (out[:, 45:50] == 0).all() and torch.isneginf(lse[:, :, 45:50]).all()
+    assert torch.isfinite(out[:, 50:]).all() and torch.isfinite(lse[:, :, 50:]).all()
+
+
+@pytest.mark.parametrize("n_split", [1, 2, 5, 0])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_fwd_split(n_split, accumulate, out_dtype):
+    q, k, v = make(13, 1, 80, 80, 300, 700, 64)  # 160 items: with n_split = 0 the last 12 are shared out
+    bad_q, bad = spoil(q, 2)
+
+    def step(x):
+        o = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+        l = torch.full((1, 80, 300), -math.inf, device=DEV)  # an empty running result
+        return cp.fwd_split(x, k, v, out=o, lse=l, accumulate=accumulate, n_split=n_split)
+
+    check(step(bad_q), step(q), bad, torch.ones_like(bad))
