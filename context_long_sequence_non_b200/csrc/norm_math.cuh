@@ -13,4 +13,9 @@ __device__ __forceinline__ float rsqrt_refined(float a) {
   return fmaf(hy, fmaf(-a * y, y, 1.0f), y);  // y + (y/2)(1 - a y^2)
 }
 
+// The factor of a row with a = mean(x^2) + eps.  An all-zero row with eps = 0 stays 0; a NaN or an
+// infinity in a row, or squares past float32, make it NaN as a whole (any test that NaN fails, such as
+// a > 0, would turn the rest of such a row into zeros).
+__device__ __forceinline__ float row_factor(float a) { return a == 0.f ? 0.f : rsqrt_refined(a); }
+
 }  // namespace cpattn

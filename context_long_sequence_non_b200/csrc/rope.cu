@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeCall c, i
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float a = ss / float(D) + c.eps;
-        const float r = a > 0.f ? rsqrt_refined(a) : 0.f;  // an all-zero row with eps = 0 stays 0
+        const float r = row_factor(a);
 #pragma unroll
         for (int u = 0; u < kRopeMaxD / 32; ++u)
           if (u * 32 + lane < D) x[u] = x[u] * r * t.gamma[index(u)] * c.out_scale;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __gr
             for (int o = 1; o < 16; o <<= 1)
               if (o < (1 << lanes_log2)) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float mean = ss * inv_d + c.eps;
-            const float r = mean > 0.f ? rsqrt_refined(mean) : 0.f;  // a zero row with eps = 0 stays 0
+            const float r = row_factor(mean);
             const float2 r2 = make_float2(r, r), os = make_float2(c.out_scale, c.out_scale);
             const float4* ga = reinterpret_cast<const float4*>(&gamma_sh[ti & 1][live ? va : 0]);
             const float4* gb = reinterpret_cast<const float4*>(&gamma_sh[ti & 1][live ? vb : 0]);

@@ -505,7 +505,7 @@ __device__ __forceinline__ uint4 rms_normalise(uint4 in, float inv_d, float eps,
 #pragma unroll
   for (int o = 1; o < kRowVec; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const float a = ss * inv_d + eps;
-  const float r = a > 0.f ? rsqrt_refined(a) : 0.f;  // an all-zero row with eps = 0 stays 0
+  const float r = row_factor(a);
   const float2 r2 = make_float2(r, r), s2 = make_float2(out_scale, out_scale);
   uint32_t w_out[4];
 #pragma unroll

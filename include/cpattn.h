@@ -336,7 +336,9 @@ CPATTN_API int cpattn_seq2head_qkv(const void* q, const void* k, const void* v, 
  * x, y : [rows][D] bf16 (a [B][S][H][D] tensor is rows = B*S*H); y may be x itself (in
  * place) but must not overlap it otherwise.  gamma : D float32 weights in device memory,
  * caller-owned.  D a power of two in [8, 256]; rows >= 0 (rows = 0 is a no-op that reads
- * no pointer, so empty tensors may pass NULL); eps >= 0 and out_scale finite.  x, y, gamma 16-byte aligned.  The sum of squares is reduced in a
+ * no pointer, so empty tensors may pass NULL); eps >= 0 and out_scale finite.  x, y, gamma 16-byte aligned.
+ * A row with a NaN or an infinity, or with squares past float32, becomes NaN; an all-zero row with
+ * eps = 0 stays 0.  The sum of squares is reduced in a
  * fixed order on the device, so y can differ from a float32 reference that sums in
  * another order by one bf16 unit in rare ties of the rounding.
  * Errors: CPATTN_ERR_NULL, _SHAPE, _ALIGN, _CUDA.

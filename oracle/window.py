@@ -99,5 +99,5 @@ def rotate(x, pos, freq, interleaved=False, factor=1.0):
 def rms_norm(x, gamma, eps=1e-6, out_scale=1.0):
     x = _f64(x)
     mean = (x * x).mean(-1, keepdims=True) + eps
-    r = np.where(mean > 0, 1.0 / np.sqrt(np.where(mean > 0, mean, 1.0)), 0.0)
+    r = np.where(mean == 0, 0.0, 1.0 / np.sqrt(np.where(mean == 0, 1.0, mean)))  # NaN stays NaN
     return x * r * _f64(gamma) * out_scale

@@ -35,7 +35,7 @@ def make(seed, B, H, Hkv, Sq, Skv, D, dtype=torch.bfloat16):
     return r(B, Sq, H, D), r(B, Skv, Hkv, D), r(B, Skv, Hkv, D)
 
 
-def spoil(q, seed):
+def spoil(q, seed, value=NAN):
     """A copy of q with NaN rows (a whole one, or one element), and bool [B][Sq][H] of them."""
     B, Sq, H, D = q.shape
     g = torch.Generator().manual_seed(seed)
@@ -45,7 +45,7 @@ def spoil(q, seed):
     at = torch.randint(0, D, (B, Sq, H), generator=g)
     hit = bad[..., None] & (whole[..., None] | (torch.arange(D) == at[..., None]))
     q = q.clone()
-    q[hit.to(DEV)] = NAN
+    q[hit.to(DEV)] = value
     return q, bad.to(DEV)
 
 
@@ -181,3 +181,58 @@ def test_fwd_split(n_split, accumulate, out_dtype):
         return cp.fwd_split(x, k, v, out=o, lse=l, accumulate=accumulate, n_split=n_split)
 
     check(step(bad_q), step(q), bad, torch.ones_like(bad))
+
+
+# ------------------------------------------------------------------ norms
+
+def spoil_rows(x, seed, value=NAN):
+    flat = x.reshape(1, -1, 1, x.shape[-1])
+    y, bad = spoil(flat, seed, value)
+    return y.reshape(x.shape), bad.reshape(x.shape[:-1])
+
+
+def check_rows(got, want, bad):
+    torch.cuda.synchronize()
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("D", [8, 64, 128, 256])
+def test_rmsnorm(D, value):
+    x, _, _ = make(17, 1, 5, 1, 40, 1, D)
+    y, bad = spoil_rows(x, D, value)
+    g = torch.ones(D, device=DEV)
+    check_rows(cp.rmsnorm(y, g), cp.rmsnorm(x, g), bad)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [NAN, math.inf])
+@pytest.mark.parametrize("D,rot", [(128, 128), (256, 64), (64, 32), (72, 20)])
+def test_qk_norm_rope(D, rot, value, dtype):
+    q, k, _ = (t[0] for t in make(18, 1, 5, 2, 40, 40, D, dtype))
+    q2, bad_q = spoil_rows(q, 1, value)
+    k2, bad_k = spoil_rows(k, 2, value)
+    g = torch.ones(D, device=DEV)
+    pos = torch.arange(40, dtype=torch.int32, device=DEV)
+    freq = cp.rope_frequencies(rot, device=DEV)[0]
+    for inter in (False, True):
+        got, want = (cp.qk_norm_rope(a, b, g, g, pos, freq, interleaved=inter) for a, b in ((q2, k2), (q, k)))
+        check_rows(got[0], want[0], bad_q)
+        check_rows(got[1], want[1], bad_k)
+
+
+@pytest.mark.parametrize("rope", [False, True])
+def test_seq2head_norm(rope):
+    P, S_l, H, D = 2, 21, 4, 64
+    q, k, v = (t.reshape(P, S_l, H, D) for t in make(19, 1, H, H, P * S_l, P * S_l, D))
+    q2, bad = spoil_rows(q, 4)
+    g = torch.ones(D, device=DEV)
+    pos = torch.arange(P * S_l, dtype=torch.int32, device=DEV)
+    freq = cp.rope_frequencies(D, device=DEV)[0]
+    step = lambda x: (cp.seq2head_qkv_norm_rope(x, k, v, P, g, g, pos, freq) if rope
+                      else cp.seq2head_qkv_norm(x, k, v, P, g, g))
+    got, want = step(q2), step(q)
+    where = cp.seq2head(bad[..., None].expand(P, S_l, H, D).bfloat16().contiguous(), P)
+    torch.cuda.synchronize()
+    check_rows(got[0], want[0], where[..., 0] == 1)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
