@@ -147,6 +147,29 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def on_stream(stream, device, make):
+    """``make()``, tensors for a call that runs on ``stream`` (None: the current one), with that stream
+    current, so that they come from its memory.  The current stream's could be memory that work queued
+    there still uses, and would go to its next allocation as soon as Python drops the tensor, both while
+    the call runs.  They are marked as used on the current stream too, where the caller reads them."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return make()
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made if isinstance(made, tuple) else (made,):
+        t.record_stream(here)
+    return made
+
+
+def _empty(stream, shape, dtype, device):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return on_stream(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device))
+
+
 def fwd(q, k, v, out=None, lse=None, scale=None, out_dtype=None, want_lse=True, stream=None):
     """Non-causal attention ``softmax(scale * Q K^T) V`` with its log-sum-exp.
 
@@ -162,9 +185,9 @@ def fwd(q, k, v, out=None, lse=None, scale=None, out_dtype=None, want_lse=True, 
     if out_dtype is None:
         out_dtype = q.dtype
     if out is None:
-        out = torch.empty((B, Sq, H, D), dtype=out_dtype, device=q.device)
+        out = _empty(stream, (B, Sq, H, D), out_dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, H, Sq), torch.float32, q.device)
     _need_shape(out, (B, Sq, H, D), "out")
     _need_shape(lse, (B, H, Sq), "lse", torch.float32)
     _need_cuda(q, k, v, out, lse)
@@ -185,9 +208,9 @@ def ulysses_fwd(q, k, v, P, out=None, lse=None, scale=None, out_dtype=None, want
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((P, S_l, H, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(stream, (P, S_l, H, D), out_dtype or q.dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((P, H // P, P * S_l), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (P, H // P, P * S_l), torch.float32, q.device)
     _need_shape(out, (P, S_l, H, D), "out")
     _need_shape(lse, (P, H // P, P * S_l), "lse", torch.float32)
     _need_cuda(q, k, v, out, lse)
@@ -213,14 +236,14 @@ def ulysses_fwd_split(q, k, v, P, out=None, lse=None, scale=None, out_dtype=None
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((P, S_l, H, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(stream, (P, S_l, H, D), out_dtype or q.dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((P, H // P, P * S_l), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (P, H // P, P * S_l), torch.float32, q.device)
     _need_shape(out, (P, S_l, H, D), "out")
     _need_shape(lse, (P, H // P, P * S_l), "lse", torch.float32)
     need = ulysses_workspace_bytes(P, S_l, H, D, out.dtype)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, (need,), torch.uint8, q.device)
     _need_cuda(q, k, v, out, lse, workspace)
     st = lib().cpattn_ulysses_fwd_split(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), P, S_l,
                                         H, D, float(scale), _dtype_code(out.dtype),
@@ -283,9 +306,9 @@ def fwd_split(q, k, v, out=None, lse=None, scale=None, out_dtype=None, accumulat
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((B_, Sq, H, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(stream, (B_, Sq, H, D), out_dtype or q.dtype, q.device)
     if lse is None:
-        lse = torch.empty((B_, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B_, H, Sq), torch.float32, q.device)
     if k.shape != (B_, Skv, H, D) or v.shape != (B_, Skv, H, D):
         raise ValueError("k and v must be [B][Skv][H][D] matching q")
     _need_shape(out, (B_, Sq, H, D), "out")
@@ -294,7 +317,7 @@ def fwd_split(q, k, v, out=None, lse=None, scale=None, out_dtype=None, accumulat
         n_split = split_suggest(B_, H, Sq, Skv)
     need = split_workspace_bytes(B_, H, Sq, D, n_split, out.dtype, Skv=Skv)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, (max(need, 256),), torch.uint8, q.device)
     _need_cuda(q, k, v, out, lse, workspace)
     st = lib().cpattn_fwd_split(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B_, H, Sq, Skv,
                                 D, float(scale), _dtype_code(out.dtype), 1 if accumulate else 0,
@@ -328,9 +351,9 @@ def merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     """Exact merge of two partial (O, LSE) results; ``out``/``lse`` may be o_a/lse_a."""
     B, S, H, D = o_a.shape
     if out is None:
-        out = torch.empty_like(o_a)
+        out = _empty(stream, o_a.shape, o_a.dtype, o_a.device)
     if lse is None:
-        lse = torch.empty_like(lse_a)
+        lse = _empty(stream, lse_a.shape, lse_a.dtype, lse_a.device)
     _need_shape(o_b, (B, S, H, D), "o_b", o_a.dtype)
     _need_shape(out, (B, S, H, D), "out", o_a.dtype)
     for name, t in (("lse_a", lse_a), ("lse_b", lse_b), ("lse", lse)):
@@ -348,7 +371,7 @@ def seq2head(src, P, out=None, stream=None):
     if P_ != P:
         raise ValueError("src.shape[0] must equal P")
     if out is None:
-        out = torch.empty((P, P * S_l, H // P, D), dtype=src.dtype, device=src.device)
+        out = _empty(stream, (P, P * S_l, H // P, D), src.dtype, src.device)
     _need_shape(out, (P, P * S_l, H // P, D), "out", src.dtype)
     _need_cuda(src, out)
     st = lib().cpattn_seq2head(_ptr(src), _ptr(out), P, S_l, H, D, src.element_size(),
@@ -363,7 +386,7 @@ def seq2head_qkv(q, k, v, P, out=None, stream=None):
     if P_ != P or k.shape != q.shape or v.shape != q.shape or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must be same-shaped [P][S_l][H][D] tensors")
     if out is None:
-        out = tuple(torch.empty((P, P * S_l, H // P, D), dtype=q.dtype, device=q.device)
+        out = tuple(_empty(stream, (P, P * S_l, H // P, D), q.dtype, q.device)
                     for _ in range(3))
     for i, t in enumerate(out):
         _need_shape(t, (P, P * S_l, H // P, D), f"out[{i}]", q.dtype)
@@ -380,7 +403,7 @@ def rmsnorm(x, gamma, eps=1e-6, out_scale=1.0, out=None, stream=None):
     if x.dtype != torch.bfloat16 or gamma.dtype != torch.float32 or gamma.shape != (x.shape[-1],):
         raise ValueError("x must be bf16 [..., D] and gamma float32 [D]")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must match x")
     _need_cuda(x, gamma, out)
@@ -403,7 +426,7 @@ def seq2head_qkv_norm(q, k, v, P, gamma_q, gamma_k, eps=1e-6, out_scale=1.0, out
         if g.dtype != torch.float32 or g.shape != (D,):
             raise ValueError("gamma_q and gamma_k must be float32 [D]")
     if out is None:
-        out = tuple(torch.empty((P, P * S_l, H // P, D), dtype=q.dtype, device=q.device)
+        out = tuple(_empty(stream, (P, P * S_l, H // P, D), q.dtype, q.device)
                     for _ in range(3))
     for i, t in enumerate(out):
         _need_shape(t, (P, P * S_l, H // P, D), f"out[{i}]", q.dtype)
@@ -422,7 +445,7 @@ def head2seq(src, P, out=None, stream=None):
         raise ValueError("src must be [P][P*S_l][Hp][D]")
     S_l, H = S_full // P, Hp * P
     if out is None:
-        out = torch.empty((P, S_l, H, D), dtype=src.dtype, device=src.device)
+        out = _empty(stream, (P, S_l, H, D), src.dtype, src.device)
     _need_shape(out, (P, S_l, H, D), "out", src.dtype)
     _need_cuda(src, out)
     st = lib().cpattn_head2seq(_ptr(src), _ptr(out), P, S_l, H, D, src.element_size(),
@@ -521,8 +544,10 @@ def _packed(t, shape, name, dtype):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _packed_like(t, dtype):
+def _packed_like(t, dtype, stream):
     """A new contiguous tensor of t's shape.  (A contiguous t's own layout will do, in half the time.)"""
+    if stream is not None:
+        return _empty(stream, t.shape, dtype, t.device)
     if t.is_contiguous():
         return torch.empty_like(t) if t.dtype == dtype else torch.empty_like(t, dtype=dtype)
     return torch.empty(t.shape, dtype=dtype, device=t.device)
@@ -538,7 +563,7 @@ def _extent(n, name):
 _CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
+def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse, stream):
     q_shape, kv_shape, dtype = q.shape, k.shape, q.dtype
     if len(q_shape) != 4 or len(kv_shape) != 4:
         raise ValueError("q, k and v must be [B][S][H][D]")
@@ -555,13 +580,16 @@ def _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse):
     if kv_len is not None:
         _packed(kv_len, (B,), "kv_len", torch.int32)
     if out is None:
-        out = _packed_like(q, out_dtype or dtype)
+        out = _packed_like(q, out_dtype or dtype, stream)
     else:
         _packed(out, q_shape, "out", out_dtype)
     if lse is not None:
         _packed(lse, (B, H, Sq), "lse", torch.float32)
     elif want_lse:
-        lse = torch.empty_strided((B, H, Sq), (H * Sq, Sq, 1), dtype=torch.float32, device=q.device)
+        if stream is None:
+            lse = torch.empty_strided((B, H, Sq), (H * Sq, Sq, 1), dtype=torch.float32, device=q.device)
+        else:
+            lse = _empty(stream, (B, H, Sq), torch.float32, q.device)
     index = _same_device(q, k, v, kv_len, out, lse)
     codes = _CODE.get(dtype), _CODE.get(out.dtype)
     if None in codes:
@@ -587,7 +615,8 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
         if not accumulate:
             raise ValueError("run is the running result of an accumulating call")
         _packed(run, q.shape, "run", torch.float32)
-    index, dims, codes, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse)
+    index, dims, codes, out, lse = _window_args(q, k, v, kv_len, out, lse, scale, out_dtype, want_lse,
+                                                stream)
     if run is not None:
         _same_device(q, run)
     _call(index, stream, _WINDOW_FWD, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -604,7 +633,7 @@ def window_decode(q, k_cache, v_cache, kv_len=None, left=-1, sinks=0, out=None, 
     window_fwd): q [B][Sq][H][D], caches [B][S_max][Hkv][D], ``kv_len`` int32 [B] the tokens each
     sequence holds, the newest included (None: S_max).  See cpattn_window_decode."""
     index, dims, codes, out, lse = _window_args(q, k_cache, v_cache, kv_len, out, lse, scale, out_dtype,
-                                                want_lse)
+                                                want_lse, stream)
     _call(index, stream, _WINDOW_DECODE, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           0 if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
           0 if lse is None else lse.data_ptr(), *dims, _extent(left, "left"), _extent(sinks, "sinks"), *codes)
@@ -671,7 +700,7 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None, stream=None):
     rows, axes, rot = _rope_args(tokens, pos, freq)
     xs = 0 if x.is_contiguous() else _token_stride(x, "x")
     if out is None:
-        out, ys = _packed_like(x, dtype), 0
+        out, ys = _packed_like(x, dtype, stream), 0
     else:
         if out.shape != shape or out.dtype != dtype:
             _need_shape(out, shape, "out", dtype)
@@ -697,7 +726,7 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, pos, freq, interleaved=False, factor=1.
     rows, axes, rot = _rope_args(tokens, pos, freq)
     qs, ks = _token_stride(q, "q"), _token_stride(k, "k")
     if out is None:
-        qo, ko, qos, kos = _packed_like(q, q.dtype), _packed_like(k, k.dtype), 0, 0
+        qo, ko, qos, kos = _packed_like(q, q.dtype, stream), _packed_like(k, k.dtype, stream), 0, 0
     else:
         qo, ko = out
         _need_shape(qo, q.shape, "out[0]", q.dtype)
@@ -730,7 +759,7 @@ def seq2head_qkv_norm_rope(q, k, v, P, gamma_q, gamma_k, pos, freq, interleaved=
         raise ValueError("pos must have a row for every token of the full sequence")
     grouped = (P, P * S_l, H // P, D)
     if out is None:
-        out = tuple(torch.empty(grouped, dtype=q.dtype, device=q.device) for _ in range(3))
+        out = tuple(_empty(stream, grouped, q.dtype, q.device) for _ in range(3))
     for i, t in enumerate(out):
         _packed(t, grouped, f"out[{i}]", q.dtype)
     for t in (q, k, v):
@@ -757,7 +786,7 @@ def selftest_wait_timeout(limit_cycles: int, stream=None):
 def selftest_exp2(t, out=None, stream=None):
     """The attention kernel's FMA-pipe 2^t on a float32 CUDA tensor (test hook)."""
     if out is None:
-        out = torch.empty_like(t)
+        out = _empty(stream, t.shape, t.dtype, t.device)
     _need_cuda(t, out)
     _check(lib().cpattn_selftest_exp2(_ptr(t), _ptr(out), t.numel(), _stream(stream)),
            "cpattn_selftest_exp2")

@@ -37,6 +37,11 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
     heads than Q; without ``acc_dtype`` the running O is float32 and rounded to q's dtype once, by
     the last chunk.  Returns ``(O, LSE)``.
     """
+    return B.on_stream(stream, q.device, lambda: _ring_step(
+        q, k_chunks, v_chunks, scale, acc_dtype, fused, n_split, stream, left, right, sinks, q_pos, k_pos))
+
+
+def _ring_step(q, k_chunks, v_chunks, scale, acc_dtype, fused, n_split, stream, left, right, sinks, q_pos, k_pos):
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[3])
     # a windowed step without an acc_dtype of the caller's keeps its running O in float32
@@ -152,9 +157,12 @@ def ulysses_attention(q_shards, k_shards, v_shards, P, scale=None, stream=None):
     """seq2head x3 -> attention per head group -> head2seq.  Returns
     ``(O [P][S_l][H][D], LSE [P][H/P][P*S_l])``."""
     P_, S_l, H, D = q_shards.shape
-    plan = UlyssesPlan(P, S_l, H, D, dtype=q_shards.dtype, device=q_shards.device)
-    out, lse = plan.run(q_shards, k_shards, v_shards, scale=scale, stream=stream)
-    return out, lse
+
+    def layer():
+        plan = UlyssesPlan(P, S_l, H, D, dtype=q_shards.dtype, device=q_shards.device)
+        return plan.run(q_shards, k_shards, v_shards, scale=scale, stream=stream)
+
+    return B.on_stream(stream, q_shards.device, layer)
 
 
 class UlyssesStreamer:
