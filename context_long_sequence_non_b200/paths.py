@@ -35,7 +35,8 @@ def ring_attention(q, k_chunks, v_chunks, scale=None, acc_dtype=None, fused=True
     ``q_pos`` on and chunk c at ``k_pos[c]`` on (None: the chunks follow one another from 0);
     every chunk is then one cpattn_window_fwd, merged in its epilogue, and K/V may have fewer
     heads than Q; without ``acc_dtype`` the running O is float32 and rounded to q's dtype once, by
-    the last chunk.  Returns ``(O, LSE)``.
+    the last chunk.  Float32 chunks are folded with the separate merge kernel, which takes rows of a
+    multiple of 16 bytes.  Returns ``(O, LSE)``.
     """
     return B.on_stream(stream, q.device, lambda: _ring_step(
         q, k_chunks, v_chunks, scale, acc_dtype, fused, n_split, stream, left, right, sinks, q_pos, k_pos))
@@ -62,6 +63,17 @@ def _ring_step(q, k_chunks, v_chunks, scale, acc_dtype, fused, n_split, stream, 
         out = torch.empty((Bn, Sq, H, D), dtype=acc_dtype, device=q.device)
         lse = torch.empty((Bn, H, Sq), dtype=torch.float32, device=q.device)
         n = len(k_chunks)
+        if q.dtype == torch.float32:  # no accumulating form
+            if n > 1 and D * out.element_size() % 16:
+                raise ValueError("a windowed ring step of float32 chunks takes rows of a multiple of 16 bytes")
+            part = (torch.empty_like(out), torch.empty_like(lse)) if n > 1 else None
+            for c, (kc, vc) in enumerate(zip(k_chunks, v_chunks)):
+                o, l = part if c > 0 else (out, lse)
+                B.window_fwd(q, kc, vc, left=left, right=right, sinks=sinks, q_pos=q_pos, k_pos=k_pos[c],
+                             out=o, lse=l, scale=scale, stream=stream)
+                if c > 0:
+                    B.merge(out, lse, o, l, out=out, lse=lse, stream=stream)
+            return out, lse
         run = torch.empty(out.shape, dtype=torch.float32, device=q.device) if rounded_once and n > 1 else out
         for c, (kc, vc) in enumerate(zip(k_chunks, v_chunks)):
             last = run is not out and c == n - 1

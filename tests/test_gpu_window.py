@@ -661,3 +661,30 @@ def test_clustered_calls_in_two_graphs():
         for got, ref in ((outs[0], want), (outs[1], want[::-1])):
             for (o, l), (ow_, lw) in zip(got, ref):
                 assert torch.equal(o, ow_) and torch.equal(l, lw)
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(4, 2, 128), (3, 3, 40), (2, 1, 256)])
+@pytest.mark.parametrize("acc_dtype", [None, torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("w", [dict(left=150, right=100, sinks=6), dict(left=-1, right=0), dict(left=70, right=0)])
+def test_f32_ring_step(acc_dtype, H, Hkv, D, w):
+    # Chunks folded by the merge kernel.  A merge's weights are e^(La - L) and e^(Lb - L): off by the LSEs'
+    # own errors, S and a few 2^-23 of |LSE| <= 16 each (1e-5 in all, with the few fp32 steps of the
+    # exponential, the quotient and the sum), so it adds (2 S + 1e-5) A; a bf16 result half a step besides.
+    q, k, v = make(40 + D, 1, H, Hkv, 260, 900, D, dtype=torch.float32)
+    cuts = [0, 1, 200, 456, 900]
+    order = [2, 0, 3, 1]
+    parts = [[x[:, a:b].contiguous().to(DEV) for a, b in zip(cuts, cuts[1:])] for x in (k, v)]
+    ks, vs = ([p[i] for i in order] for p in parts)
+    out, lse = cp.ring_attention(q.to(DEV), ks, vs, acc_dtype=acc_dtype, q_pos=300, k_pos=[cuts[i] for i in order], **w)
+    torch.cuda.synchronize()
+    assert out.dtype == (acc_dtype or torch.float32)
+    o_ref, l_ref, a = ow.window_attention(q, k, v, D ** -0.5, q_pos=300, **w)
+    S = logit_error(q, k, D ** -0.5)
+    bound = (2e-6 + 2 * S + 900 * 2.0 ** -24 + 3 * (2 * S + 1e-5)) * a
+    if acc_dtype == torch.bfloat16:
+        bound = bound + 4 * HALF * (a + bound)
+    assert (np.abs(_f64(out) - o_ref) <= bound + 2.0 ** -24 * np.abs(o_ref) + 1e-30).all()
+    empty = np.isneginf(l_ref)
+    assert np.array_equal(np.isneginf(_f64(lse)), empty)
+    err = np.abs(_f64(lse) - np.where(empty, 0, l_ref))[~empty]
+    assert (err <= 4 * (S + 2e-5 + 2.0 ** -22 * np.abs(l_ref[~empty]))).all()

@@ -330,3 +330,34 @@ def test_calls_by_number_match_the_declared_arguments(L):
         assert L.cpattn_call(e.code, None, e.n) == B.ERR_NULL
     for code in (-1, 5, 1 << 30):
         assert L.cpattn_call(code, zero, 4) == B.ERR_SHAPE
+
+
+# ------------------------------------------------------------------ ring step, float32
+
+def test_float32_windowed_ring_step_folds_its_chunks_with_merge(monkeypatch):
+    # the accumulating windowed call takes bf16 only: every chunk is a call of its own, then a merge
+    calls = []
+    monkeypatch.setattr(B, "window_fwd", lambda *a, **kw: calls.append(("window", kw["out"], kw.get("accumulate", False))))
+    monkeypatch.setattr(B, "merge", lambda *a, **kw: calls.append(("merge", a[0], kw["out"])))
+    q, k = t(1, 5, 4, 64, dtype=torch.float32), t(1, 6, 2, 64, dtype=torch.float32)
+    for acc_dtype in (None, torch.float32, bf):
+        calls.clear()
+        out, _ = cp.ring_attention(q, [k, k, k], [k, k, k], left=3, acc_dtype=acc_dtype)
+        assert out.dtype == (acc_dtype or torch.float32)
+        assert [c[0] for c in calls] == ["window", "window", "merge", "window", "merge"]
+        assert calls[0][1] is out and all(c[1] is out and c[2] is out for c in calls if c[0] == "merge")
+        assert not any(c[2] for c in calls if c[0] == "window")
+    calls.clear()
+    cp.ring_attention(q, [k], [k], left=3)
+    assert [c[0] for c in calls] == ["window"]
+
+
+def test_float32_windowed_ring_step_refuses_rows_that_merge_does_not_take(monkeypatch):
+    def launch(*a, **kw):
+        raise AssertionError("launched")
+
+    monkeypatch.setattr(B, "window_fwd", launch)
+    for D, acc_dtype in ((30, None), (7, torch.float32), (44, bf)):
+        q, k = t(1, 5, 4, D, dtype=torch.float32), t(1, 6, 2, D, dtype=torch.float32)
+        with pytest.raises(ValueError, match="16 bytes"):
+            cp.ring_attention(q, [k, k], [k, k], left=3, acc_dtype=acc_dtype)
