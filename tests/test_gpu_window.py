@@ -11,6 +11,7 @@ The fp32 kernel has no rounding to bf16: |O err| <= (2e-6 + 2S + n 2^-24) A over
 """
 
 import math
+import warnings
 
 import numpy as np
 import pytest
@@ -688,3 +689,92 @@ def test_f32_ring_step(acc_dtype, H, Hkv, D, w):
     assert np.array_equal(np.isneginf(_f64(lse)), empty)
     err = np.abs(_f64(lse) - np.where(empty, 0, l_ref))[~empty]
     assert (err <= 4 * (S + 2e-5 + 2.0 ** -22 * np.abs(l_ref[~empty]))).all()
+
+
+# ------------------------------------------------------------------ which kernel serves a decode call
+
+def kernel_of(call, tmp_path):
+    """The windowed kernel that a call launches, by its captured graph's dump."""
+    call()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    g.enable_debug_mode()
+    with torch.cuda.graph(g):
+        call()
+    dump = tmp_path / "graph.dot"
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")  # it announces itself
+        g.debug_dump(str(dump))
+    text = dump.read_text()
+    found = [n for n in ("window_sm100_kernel", "window_decode_kernel", "window_f32_kernel") if n in text]
+    assert len(found) == 1, found
+    return found[0]
+
+
+def decode_served_by(kernel, tmp_path, B, H, Hkv, Sq, S, D, **w):
+    q, k, v = make(B + Sq + S, B, H, Hkv, Sq, S, D)
+    kv_len = [S, 20, 0, Sq, S // 2, 1, S - 7, Sq - 1, Sq + 1][:B]
+    kv_len = [max(0, n) for n in kv_len] + [S - 31 * b for b in range(len(kv_len), B)]
+    for b, n in enumerate(kv_len):
+        k[b, n:] = float("nan")
+        v[b, n:] = float("inf")
+    lens = torch.tensor(kv_len, dtype=torch.int32, device=DEV)
+    qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
+    assert kernel_of(lambda: cp.window_decode(qd, kd, vd, lens, **w), tmp_path) == kernel
+    o, l = run_decode(q, k, v, kv_len, **w)
+    o2, l2 = run_decode(q, k, v, kv_len, **w)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+    run_decode(q, k, v, kv_len, out_dtype=torch.float32, **w)
+
+
+# Sizes where the time to expect of the split kernel is 1.3 to 4 times that of the tiles: heads that share a
+# tile (1, 4, 8 and 16 of them), tiles of their own and tiles in clusters, batches with empty sequences.
+@pytest.mark.parametrize("B,H,Hkv,Sq,S,D", [(8, 32, 8, 32, 2000, 64), (8, 64, 4, 48, 2500, 64), (1, 128, 8, 64, 2500, 64),
+                                            (16, 24, 24, 70, 1500, 64), (2, 8, 1, 300, 4000, 64), (4, 60, 12, 130, 1999, 64),
+                                            (8, 32, 8, 32, 2000, 128), (3, 64, 4, 60, 1500, 128)])
+@pytest.mark.parametrize("w", [dict(left=-1), dict(left=1200, sinks=70)])
+def test_decode_on_the_tiles(B, H, Hkv, Sq, S, D, w, tmp_path):
+    decode_served_by("window_sm100_kernel", tmp_path, B, H, Hkv, Sq, S, D, **w)
+
+
+@pytest.mark.parametrize("B,H,Hkv,Sq,S,D", [(3, 8, 2, 1, 700, 128), (8, 16, 16, 4, 1990, 64), (16, 32, 8, 1, 900, 64),
+                                            (1, 16, 16, 9, 3000, 128)])
+@pytest.mark.parametrize("w", [dict(left=-1), dict(left=1200, sinks=70)])
+def test_decode_on_the_split_kernel(B, H, Hkv, Sq, S, D, w, tmp_path):
+    decode_served_by("window_decode_kernel", tmp_path, B, H, Hkv, Sq, S, D, **w)
+
+
+# ------------------------------------------------------------------ a float32 running O, rounded once
+
+def check_rounded_once(out, lse, ref, q, k, merges):
+    """A single pass's bound plus the fp32 steps of the merges: O is off by the weights' error of each chunk
+    (shares of A that sum to it), a few fp32 steps a merge, and one half-step of the result."""
+    o_ref, l_ref, a = ref
+    assert out.dtype == torch.bfloat16
+    S = logit_error(q, k, q.shape[-1] ** -0.5)
+    bound = (HALF + 2e-5 + 2 * S + merges * 1e-6) * a
+    assert (np.abs(_f64(out) - o_ref) <= bound + HALF * (np.abs(o_ref) + bound) + 1e-30).all()
+    empty = np.isneginf(l_ref)
+    l = _f64(lse)
+    assert np.array_equal(np.isneginf(l), empty)
+    err = np.abs(l - np.where(empty, 0, l_ref))[~empty]
+    assert (err <= S + 2e-5 + (1 + merges) * 2.0 ** -22 * np.abs(l_ref[~empty])).all()
+
+
+@pytest.mark.parametrize("B,H,Hkv,Sq,Skv,D", [(1, 1, 1, 1, 4000, 128), (1, 2, 1, 130, 2000, 64), (2, 3, 3, 300, 900, 128),
+                                              (1, 10, 2, 128, 1500, 64), (1, 40, 8, 190, 1100, 128),
+                                              (1, 24, 4, 800, 700, 128), (2, 12, 12, 890, 500, 64),
+                                              (2, 64, 1, 5, 700, 64), (1, 128, 1, 130, 260, 128), (1, 27, 3, 37, 90, 64)])
+@pytest.mark.parametrize("w", [dict(left=-1, right=-1), dict(left=300, right=0, sinks=70), dict(left=60, right=2, sinks=3)])
+def test_merges_of_a_float32_running_result_round_once(B, H, Hkv, Sq, Skv, D, w):
+    q, k, v = make(50 + Sq, B, H, Hkv, Sq, Skv, D)
+    at = max(Skv - Sq, 0)
+    cuts = [0, Skv // 2 + 3, Skv - 5, Skv]
+    run = torch.empty(q.shape, device=DEV)
+    out, lse = torch.empty_like(q, device=DEV), torch.empty((B, H, Sq), device=DEV)
+    for c in range(3):
+        kc, vc = (x[:, cuts[c]:cuts[c + 1]].contiguous().to(DEV) for x in (k, v))
+        last = c == 2
+        cp.window_fwd(q.to(DEV), kc, vc, out=out if last else run, run=run if last else None, lse=lse,
+                      accumulate=c > 0, q_pos=at, k_pos=cuts[c], **w)
+    torch.cuda.synchronize()
+    check_rounded_once(out, lse, ow.window_attention(q, k, v, D ** -0.5, q_pos=at, **w), q, k, 2)
