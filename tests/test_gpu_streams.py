@@ -108,3 +108,42 @@ def test_results_dropped_while_the_current_stream_reads_them():
         junk()
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+def test_captured_compositions_follow_their_inputs():
+    # ring steps with a window (their temporaries in the graph's memory) and a Ulysses layer with norm, rotation
+    # and window, in two graphs replayed beside one another
+    P, S_l, H, D = 2, 150, 8, 128
+    q, k, v = make(5, *[(1, 300, H, D)] * 3)
+    s = make(6, *[(P, S_l, H, D)] * 3)
+    f = [t.float() for t in (q, k, v)]
+    pos = torch.arange(P * S_l, dtype=torch.int32, device=DEV)
+    gam = torch.ones(D, device=DEV)
+    plans = [cp.UlyssesPlan(P, S_l, H, D, qk_norm=(gam, gam), rope=(pos, cp.rope_frequencies(D, device=DEV)[0]),
+                            window=(60, 20, 4)) for _ in range(2)]
+
+    def step(plan):
+        ring = lambda a, b, c, **kw: cp.ring_attention(a, [b[:, :100], b[:, 100:]], [c[:, :100], c[:, 100:]], left=90,
+                                                       right=30, sinks=3, **kw)
+        return [*ring(q, k, v), *ring(q, k, v, acc_dtype=torch.float32), *ring(*f), *plan.run(*s)]
+
+    graphs, outs = [], []
+    step(plans[0])
+    for plan in plans:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(plan))
+        graphs.append(g)
+    fresh = cp.UlyssesPlan(P, S_l, H, D, qk_norm=(gam, gam), rope=plans[0].rope, window=(60, 20, 4))
+    for seed in range(2):
+        for t in (q, k, v, *s, *f):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(seed + t.numel() % 7)))
+        want = [t.clone() for t in step(fresh)]
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        for got in outs:
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
