@@ -2,8 +2,9 @@
 //
 // A block takes 8, 32 or 48 (token, head) rows of one key head and walks the keys that some row of
 // them sees -- early (sink) keys, then the window, as one list -- 64 at a time: S = Q K^T, the online
-// softmax in base 2 and O += P V, all in fp32 (fp32 has no tensor-core product that keeps its
-// digits).  Keys of the list that a row does not see weigh exactly 0; keys outside the list are
+// softmax in base 2 and O += P V, all in fp32.  (The tensor cores take fp32 digits only in parts, such as
+// three bf16 numbers an operand and six products for one; that form was not built or measured.)
+// Keys of the list that a row does not see weigh exactly 0; keys outside the list are
 // never read.  D is padded to 64, 128 or 256 with zeros.
 //
 // Layout.  A warp holds R rows and a lane two of the 64 keys of S and D / 32 columns of O.  The
@@ -20,7 +21,10 @@
 // Split.  A cluster of up to 8 blocks shares the key list of one row tile where the tiles alone
 // leave SMs idle; the parts (m, l, O) are folded through distributed shared memory in a fixed order.
 // One token x 8 heads, 8192 keys of 128: 36 us (827 with neither the split nor one-row warps).
-// Measured besides: 3000 x 8 heads of 128, 800 keys before and 100 after, 316 us = 35 TFLOP/s.
+// Measured besides: 3000 x 8 heads of 128, 800 keys before and 100 after, 316 us = 31 TFLOP/s of visible
+// products (its form, six rows a warp at D = 128, spills 8 bytes); 16 sequences x 32 heads on 8, one
+// token, 2048 keys, 65 us = 4.2 TB/s; one token x 8 heads, 8192 keys, 1.9 TB/s: 64 blocks of 16 chunks of
+// 64 keys, each chunk's copy, S, softmax and P V one behind another.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -8,12 +8,12 @@
 // rescale_log2, so that most blocks rescale nothing.
 //
 // One CTA takes 128 query rows -- tokens of one (b, h), or fewer tokens of 2, 4, .. heads that share a
-// key head -- and two CTAs share an SM.  Windows are short -- ten
-// to forty blocks of 128 -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue
+// key head -- and two CTAs share an SM.  Windows are short -- twenty to seventy
+// blocks -- so a CTA's start (barriers, TMEM, the first loads) and its epilogue
 // would be a large share of its life if nothing ran beside them; with two independent CTAs one's
 // softmax, start and end overlap the other's matrix products, and a tile visits its own key
 // blocks and no neighbour's.  The price, K and V not shared between two query tiles, is L2
-// traffic of 64 KB per 128 x 128 products, under half of what L2 delivers.  Blocks start at the
+// traffic of 32 KB per 128 x 64 products, under half of what L2 delivers.  Blocks start at the
 // first key that the tile sees, not at a multiple of 64: a window of 4096 costs 66 of them.
 //   warps 0-3  softmax, one thread per query row = TMEM lane
 //   warp  4    TMA producer: Q, then per block K into one ring and V into another; the first
@@ -39,8 +39,12 @@
 // 100 for P's stores, 300 to the next S; the tensor pipe is busy about 60% of the time.  Moving a
 // share of the exponentials to the FMA pipe (1, 2 or 3 of 8, a polynomial) changes nothing.  At the
 // large sizes the card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x
-// 16 heads, causal window 4096 with 64 sinks, 1.42 ms = 1010 TFLOP/s of visible products;
-// 4608 x 24, 512 to either side with 512 sinks, 97 us = 815 TFLOP/s.  Tried and not kept, on the
+// 16 heads, causal window 4096 with 64 sinks, 1.41 to 1.47 ms = 974 to 1015 TFLOP/s of visible products
+// (heads of 64: 1.05 ms = 684); 4608 x 24, 512 to either side with 512 sinks, 97 us = 815 (heads of 64: 75 us
+// = 525).  More softmax warps are not what is missing: the dense kernel (attn_sm100.cu) has as many an SM
+// and the same exponentials, and takes 13.2 ms where this one takes 17.0 on 44160 x 16 heads without bounds.
+// It has N = 128 products, hands P over in halves, and 216 registers a softmax thread.
+// Tried and not kept, on the
 // 128-key form: two 128-row tiles in one CTA with shared K and V, one CTA per item (2% slower on
 // the first case, 40% at 333 rows) and persistent over items (19% slower).
 //
@@ -65,8 +69,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kBlockM = 128;
 constexpr int kBlockN = 64;
-// Six warps: two CTAs per SM then have 168 registers a thread, which holds a row's 128 logits
-// (a 224-thread CTA would have 144, a 256-thread one 128).
+// Six warps: two CTAs per SM then have 168 registers a thread (a 224-thread CTA would have 144, a
+// 256-thread one 128).  Writing forms use 115 to 119 of them, merging ones 123 to 163; merging into fp32 at D = 128, whose threads
+// hold 16 vectors of the running O beside a row's 64 logits, spills 24 bytes.
 constexpr int kThreads = 192;
 constexpr int kWarpProducer = 4, kWarpMma = 5;
 constexpr uint32_t kTmemCols = 256;
@@ -831,12 +836,6 @@ bool encode(CUtensorMap* map, const void* ptr, int B, int S, int H, int D, long 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks that share a query tile's keys, and the time (us) that the kernel is then expected to take.  A
-// tile walks 0.66 us per block of 64 keys, 0.95 beside another on its SM; parts cost 1.9 us to
-// start and fold, 4 when they are more than the SMs.  Clusters of four and eight do not fill
-// every SM.  Measured, parts 1 / 2 / 4 / 8: 20 tiles of 512 keys 9.9 / 9.2 / 7.9 / 10.3 us, of 2048
-// 25.8 / 17.5 / 12.6 / 14.1; 100 tiles of 1024 15.7 / 16.2 (200 blocks), of 4096 47.6 / 38.2; 48 tiles of
-// 2048 26.5 / 18.5 / 18.1; 37 tiles of 512 10.1 / 9.4 / 10.7 / 16.9.
 // Heads of a key head that a tile takes together, as a power of two.  Tokens then span fewer keys and
 // few of them still fill a tile: 16000 x 32 heads on 8, causal window 2000, 579 -> 530 us, 4000 x 32 on
 // 8, window 100, 40 -> 34.5; 16 tokens of 8 sequences x 32 heads on 8 against 4096 keys 77 -> 35.
@@ -851,6 +850,12 @@ long long tiles(const WindowCall& c, int lg) {
   return ((long long)c.Sq + n - 1) / n * (c.H >> lg) * c.B;
 }
 
+// Blocks that share a query tile's keys, and the time (us) that the kernel is then expected to take.  A
+// tile walks 0.66 us per block of 64 keys, 0.95 beside another on its SM; parts cost 1.9 us to
+// start and fold, 4 when they are more than the SMs.  Clusters of four and eight do not fill
+// every SM.  Measured, parts 1 / 2 / 4 / 8: 20 tiles of 512 keys 9.9 / 9.2 / 7.9 / 10.3 us, of 2048
+// 25.8 / 17.5 / 12.6 / 14.1; 100 tiles of 1024 15.7 / 16.2 (200 blocks), of 4096 47.6 / 38.2; 48 tiles of
+// 2048 26.5 / 18.5 / 18.1; 37 tiles of 512 10.1 / 9.4 / 10.7 / 16.9.
 struct Plan {
   int parts;
   double us;
