@@ -606,7 +606,7 @@ def window_fwd(q, k, v, left=-1, right=-1, sinks=0, q_pos=0, k_pos=0, kv_len=Non
 
     q: [B][Sq][H][D], k/v: [B][Skv][Hkv][D] with H a multiple of Hkv (bf16 -> tensor-core kernel,
     D 64 or 128; fp32 -> CUDA-core kernel, D <= 256); their heads may be slices of a wider row.
-    ``kv_len``: int32 [B], keys of each sequence.  ``accumulate`` merges into the running
+    ``kv_len``: int32 [B], keys of each sequence.  ``accumulate`` (bf16) merges into the running
     (out, lse), or merges the running (``run`` float32, lse) into a bf16 ``out``.
     Returns ``(out [B][Sq][H][D], lse [B][H][Sq] float32)``."""
     if accumulate and (lse is None or (out is None and run is None)):

@@ -39,7 +39,7 @@
 // 100 for P's stores, 300 to the next S; the tensor pipe is busy about 60% of the time.  Moving a
 // share of the exponentials to the FMA pipe (1, 2 or 3 of 8, a polynomial) changes nothing.  At the
 // large sizes the card is at its power cap besides (1.4 to 1.55 GHz).  Measured: 44160 tokens x
-// 16 heads, causal window 4096 with 64 sinks, 1.41 to 1.47 ms = 974 to 1015 TFLOP/s of visible products
+// 16 heads, causal window 4096 with 64 sinks, 1.41 to 1.49 ms = 962 to 1017 TFLOP/s of visible products
 // (heads of 64: 1.05 ms = 684); 4608 x 24, 512 to either side with 512 sinks, 97 us = 815 (heads of 64: 75 us
 // = 525).  More softmax warps are not what is missing: the dense kernel (attn_sm100.cu) has as many an SM
 // and the same exponentials, and takes 13.2 ms where this one takes 17.0 on 44160 x 16 heads without bounds.

@@ -147,3 +147,35 @@ def test_captured_compositions_follow_their_inputs():
         for got in outs:
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
+
+
+def test_calls_on_a_side_stream_of_a_capture():
+    # the side stream joins the capture; what the calls allocate there is the graph's, dropped results among it
+    q, k, v = make(9, (1, 300, 8, 128), (1, 900, 8, 128), (1, 900, 8, 128))
+    ks, vs = ([t[:, a:a + 300].contiguous() for a in (0, 300, 600)] for t in (k, v))
+    w = dict(left=200, right=50, sinks=4, q_pos=300)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        a = cp.ring_attention(q, ks, vs, stream=side, **w)
+        cp.window_fwd(q, k, v, stream=side, **w)
+        b = cp.window_fwd(q, k, v, stream=side, **w)[0]
+        here.wait_stream(side)
+        c = cp.rmsnorm(b, torch.ones(128, device=DEV))
+        return [*a, b, c]
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(7)
+        g.replay()
+        junk()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
